@@ -32,12 +32,16 @@ __device__ inline float bits_f32(unsigned u) { return __builtin_bit_cast(float, 
 
 struct Bf16 {
     using type = __bf16;
+    static constexpr bool IS_BF16 = true;
+    static constexpr unsigned EXP = 0x7f80u;               // exponent bits: all set = not finite
     __device__ static inline float lo(unsigned w) { return bits_f32(w << 16); }
     __device__ static inline float hi(unsigned w) { return bits_f32(w & 0xffff0000u); }
 };
 
 struct F16 {
     using type = _Float16;
+    static constexpr bool IS_BF16 = false;
+    static constexpr unsigned EXP = 0x7c00u;
     __device__ static inline float lo(unsigned w) {
         return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<unsigned short>(w)));
     }
@@ -151,6 +155,53 @@ __global__ __launch_bounds__(NTA) void append_kernel(AppendParams A) {
 }
 
 // ------------------------------------------------------------------ attention
+//
+// For one batch row and cache head the R * G query rows (R tokens, G query heads that
+// share the cache head) all read the same keys and values, so the cache crosses HBM
+// once while every row is computed from it on the matrix cores; the kernel is bound by
+// that stream (at R * G = 24, D = 128 the products need less than a tenth of their
+// peak while HBM is saturated).
+//
+// With X = K Q^T as 16 x 16 tiles (keys are the MFMA's A operand), lane l holds scores
+// of ONE query row (l % 16) for keys 4 (l / 16) + 0..3 of the tile: the softmax is
+// arithmetic within the lane. Two such tiles (32 keys) give, in the same registers,
+// the B operand of O^T = V^T P^T, if the contraction takes the keys in the order
+// {4g..4g+3, 16+4g..16+4g+3} for lane group g; the A operand, columns of V in that
+// order, comes from LDS by transposing reads (ds_read_b64_tr_b16, or _tr_b8 for e4m3).
+// No score or weight ever crosses lanes. The running maximum of a row moves only when
+// a score exceeds it by more than 2^8 in weight (checked by a vote), so the two
+// exchanges and the rescaling that go with a new maximum are rare; weights are then
+// at most 2^8, and sums and accumulators are float32.
+//
+// Each of a workgroup's four waves walks its own tiles of 32 keys with its own
+// accumulators, through its own part of LDS, and never waits for another wave: keys
+// and values go from memory straight into LDS (16 bytes per lane, the lane fetching
+// the chunk that belongs at its place, see `chunk`), the next tile's keys in flight
+// during the softmax and the product with V, its values during the product with K.
+// The waves' results are joined through LDS at the end.
+//
+// Split over the length: the batch's sequences are cut into units of 128 keys, and W
+// workgroups per cache head (together one resident round) take equal, contiguous
+// ranges of the units, whatever the lengths are; the ranges are found on the device
+// from kv_len. A sequence inside one range is finished there. Of a sequence that
+// crosses ranges each workgroup leaves its unnormalised result and statistics in the
+// workspace (at most two such pieces per workgroup: the first and the last of its
+// range), and join_kernel merges them.
+
+constexpr int NTQ = 256;
+constexpr int NWQ = NTQ / 64;
+constexpr int TT = 32;                                     // keys of a wave's tile
+constexpr int TU = TT * NWQ;                               // keys of a unit
+constexpr int CUS = 256;
+constexpr float LAZY = 8.0f;                               // log2 of the largest weight
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef __attribute__((address_space(3))) i16x4* lds_i16x4;
+typedef __attribute__((address_space(3))) i32x2* lds_i32x2;
+typedef __attribute__((address_space(1))) const void* glb_ptr;
 
 struct AttnParams {
     Cache c;
@@ -158,81 +209,559 @@ struct AttnParams {
     long long qs[3];           // bytes between batch rows, tokens, heads
     const float* slopes;       // [Hq] or null
     char* out;                 // [B, R, Hq, D]
+    float* ws;                 // per (w, lane): two slots of M16 * (D + 2) floats
     float scale, softcap;
-    int window, Hq, G;
+    int window, Hq, G, D;
+    int M;                     // R * G query rows per cache head
+    int MB;                    // row blocks of M16 = 16 * MT rows
+    int M16;
+    int W;                     // workgroups per cache head and row block
+    int direct;                // join_kernel: one workgroup per batch row (else per range border)
 };
 
-constexpr int NTQ = 256;
+// a batch row's keys: positions [lo, hi) are seen by some token in use
+struct Seq {
+    int kv, n;                 // first new position, tokens in use (0: bad lengths)
+    int lo, hi, base;          // base: lo rounded down to a tile
+    int units;
+};
 
-// One workgroup per query row: scores of 256 tokens at a time, one per thread,
-// then one output element per thread.
-template <class T, int D, bool E4M3>
-__global__ __launch_bounds__(NTQ) void attn_kernel(AttnParams A) {
-    const Cache& C = A.c;
-    __shared__ float q[D], p[NTQ], red[NTQ];
-    __shared__ const char* vrow[NTQ];
-    __shared__ int bad;
-    const int t = static_cast<int>(threadIdx.x);
-    const int hq = static_cast<int>(blockIdx.x) % A.Hq, bi = static_cast<int>(blockIdx.x) / A.Hq;
-    const int b = bi / C.R, i = bi % C.R, h = hq / A.G;
-    typename T::type* out = reinterpret_cast<typename T::type*>(A.out) + static_cast<long long>(blockIdx.x) * D;
-    int kv;
-    const int n = seq_rows(C, b, kv);
-    if (i >= n) {
-        if (t < D) out[t] = static_cast<typename T::type>(n ? 0.0f : NAN);
-        return;
+__device__ inline Seq seq_of(const AttnParams& A, int b) {
+    Seq s;
+    s.n = seq_rows(A.c, b, s.kv);
+    if (s.n == 0) { s.lo = s.hi = s.base = 0; s.units = 1; return s; }
+    s.lo = A.window > 0 ? max(0, s.kv + 1 - A.window) : 0;
+    s.hi = s.kv + s.n;
+    s.base = s.lo & ~(TT - 1);
+    s.units = (s.hi - s.base + TU - 1) / TU;
+    return s;
+}
+
+struct Plan {
+    long long wave[NWQ];
+    long long total, pre;
+    int b;
+};
+
+__device__ inline long long wave_inclusive(long long v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const long long u = __shfl_up(v, d, 64);
+        if (lane >= d) v += u;
     }
-    const int pos = kv + i, lo = A.window > 0 ? max(0, pos + 1 - A.window) : 0;
-    if (t == 0) bad = 0;
-    if (t < D)
-        q[t] = static_cast<float>(reinterpret_cast<const typename T::type*>(A.q + b * A.qs[0] + i * A.qs[1] +
-                                                                             hq * A.qs[2])[t]);
+    return v;
+}
+
+// Inclusive scan over the workgroup of v; total is its sum. Ends with a barrier.
+__device__ inline long long block_inclusive(Plan& P, long long v, long long& total) {
+    const int w = threadIdx.x >> 6;
+    const long long x = wave_inclusive(v);
+    if ((threadIdx.x & 63) == 63) P.wave[w] = x;
     __syncthreads();
-    const float ksc = E4M3 ? C.k_scale[h] : 1.0f, vsc = E4M3 ? C.v_scale[h] : 1.0f;
-    auto value = [&](const char* row, int j) -> float {
-        if constexpr (E4M3) {
-            typedef __bf16 v2 __attribute__((ext_vector_type(2)));
-            const v2 f = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(reinterpret_cast<const unsigned char*>(row)[j],
-                                                                   1.0f, false);
-            return static_cast<float>(f.x);
-        } else {
-            return static_cast<float>(reinterpret_cast<const typename T::type*>(row)[j]);
-        }
-    };
-    float m = -F32_MAX, l = 0.0f, o = 0.0f;
-    for (int t0 = lo; t0 <= pos; t0 += NTQ) {
-        const int tok = t0 + t;
-        float x = -INFINITY;
-        if (tok <= pos) {
-            int page = C.table[static_cast<long long>(b) * C.max_pages + (tok >> C.shift)];
-            if (!page_ok(C, page)) { bad = 1; page = 0; }
-            const int slot = tok & ((1 << C.shift) - 1);
-            const char* krow = C.k + page * C.ks[0] + h * C.ks[1] + slot * C.ks[2];
-            vrow[t] = C.v + page * C.vs[0] + h * C.vs[1] + slot * C.vs[2];
-            float s = 0.0f;
-            for (int j = 0; j < D; ++j) s += q[j] * value(krow, j);
-            x = s * A.scale * ksc;
-            if (A.softcap > 0.0f) x = A.softcap * tanhf(x / A.softcap);
-            if (A.slopes) x += A.slopes[hq] * static_cast<float>(tok - pos);
-        }
-        red[t] = x;
-        __syncthreads();
-        float mx = m;
-        for (int j = 0; j < NTQ; ++j) mx = fmaxf(mx, red[j]);
-        const float e = exp2f((x - mx) * LOG2E), r = exp2f((m - mx) * LOG2E);
-        p[t] = x == -INFINITY && tok > pos ? 0.0f : e;
-        m = mx;
-        __syncthreads();
-        l *= r;
-        o *= r;
-        const int cnt = min(NTQ, pos + 1 - t0);
-        for (int j = 0; j < cnt; ++j) {
-            l += p[j];
-            if (t < D) o += p[j] * value(vrow[j], t);
-        }
-        __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int j = 0; j < NWQ; ++j) {
+        if (j < w) before += P.wave[j];
+        total += P.wave[j];
     }
-    if (t < D) out[t] = static_cast<typename T::type>(bad ? NAN : o / l * vsc);
+    __syncthreads();
+    return before + x;
+}
+
+// Units of all batch rows, and of those before batch row `stop`.
+__device__ inline long long units_total(const AttnParams& A, Plan& P, int stop, long long& before) {
+    const int t = static_cast<int>(threadIdx.x);
+    long long all = 0, pre = 0;
+    for (int b = t; b < A.c.B; b += NTQ) {
+        const int u = seq_of(A, b).units;
+        all += u;
+        if (b < stop) pre += u;
+    }
+    long long total;
+    block_inclusive(P, pre, before);
+    block_inclusive(P, all, total);
+    return total;
+}
+
+// The batch row that holds unit `target` (< the total) and the units before it.
+__device__ inline int units_find(const AttnParams& A, Plan& P, long long target, long long& pre) {
+    const int t = static_cast<int>(threadIdx.x);
+    long long run = 0;
+    for (int b0 = 0; b0 < A.c.B; b0 += NTQ) {
+        const int u = b0 + t < A.c.B ? seq_of(A, b0 + t).units : 0;
+        long long total;
+        const long long inc = run + block_inclusive(P, u, total);
+        if (target >= inc - u && target < inc) { P.b = b0 + t; P.pre = inc - u; }
+        run += total;
+        if (target < run) break;
+    }
+    __syncthreads();
+    pre = P.pre;
+    const int b = P.b;
+    __syncthreads();
+    return b;
+}
+
+__device__ inline long long range_start(const AttnParams& A, long long total, int w) { return total * w / A.W; }
+
+// s_waitcnt: at most `vm` loads in flight / no LDS read in flight; nothing moves across
+template <int VM>
+__device__ inline void wait_loads() {
+    static_assert(VM <= 63, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4) | (15 << 8));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+__device__ inline void wait_lds() {
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <class T>
+__device__ inline f32x4 mfma(i32x4 a, i32x4 b, f32x4 c) {
+    typedef typename T::type v8 __attribute__((ext_vector_type(8)));
+    if constexpr (T::IS_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+}
+
+// eight e4m3 codes to eight values of T (exact: T has more exponents and bits)
+template <class T>
+__device__ inline i32x4 widen8(i32x2 w) {
+    typedef typename T::type v2 __attribute__((ext_vector_type(2)));
+    i32x4 o;
+    if constexpr (T::IS_BF16) {
+        o.x = __builtin_bit_cast(int, (v2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x, 1.0f, false));
+        o.y = __builtin_bit_cast(int, (v2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x, 1.0f, true));
+        o.z = __builtin_bit_cast(int, (v2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.y, 1.0f, false));
+        o.w = __builtin_bit_cast(int, (v2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.y, 1.0f, true));
+    } else {
+        o.x = __builtin_bit_cast(int, (v2)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, 1.0f, false));
+        o.y = __builtin_bit_cast(int, (v2)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.x, 1.0f, true));
+        o.z = __builtin_bit_cast(int, (v2)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, 1.0f, false));
+        o.w = __builtin_bit_cast(int, (v2)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w.y, 1.0f, true));
+    }
+    return o;
+}
+
+template <int D, bool E4M3>
+struct TileShape {
+    static constexpr int RB = D * (E4M3 ? 1 : 2);          // bytes of a row (one key or value)
+    static constexpr int CPR = RB / 16;                    // 16-byte chunks of a row
+    static constexpr int RPI = 64 / CPR;                   // rows one load instruction of a wave fills
+    static constexpr int NL = TT / RPI;                    // load instructions per tile
+    static constexpr int KB = TT * RB;                     // bytes of a tile
+    static constexpr int LDS = NWQ * 2 * KB;
+    // Row r's chunk c sits at place c ^ swz(r), so that the 16 lanes that read one
+    // chunk of 16 consecutive rows touch 16 different 16-byte columns of the banks.
+    __device__ static inline int swz(int r) {
+        return CPR >= 16 ? r & 15 : CPR == 8 ? (r >> 1) & 7 : (r >> 2) & 3;
+    }
+};
+
+// workgroups per CU: as many as LDS and about 512 / 4 .. 512 registers per lane allow
+template <int D, int MT, bool E4M3>
+constexpr int attn_occupancy() {
+    constexpr int lds = 160 * 1024 / (TileShape<D, E4M3>::LDS + 3 * 1024);
+    constexpr int regs = MT * D <= 128 ? 4 : MT * D <= 192 ? 3 : MT * D <= 512 ? 2 : 1;
+    return lds < regs ? lds : regs;
+}
+
+template <class T, int D, int MT, bool E4M3>
+__global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_kernel(AttnParams A) {
+    using S = TileShape<D, E4M3>;
+    constexpr int M16 = 16 * MT, ND = D / 16, NC = D / 32;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[S::LDS];
+    __shared__ float st_m[NWQ][M16], st_l[NWQ][M16], fin[M16];
+    __shared__ Plan plan;
+    const Cache& C = A.c;
+    const int t = static_cast<int>(threadIdx.x), lane = t & 63, wv = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+    // the MB row blocks of one range read the same keys: workgroups 8 apart, on one XCD
+    const int per = 8 * A.MB, sub = static_cast<int>(blockIdx.x) % per;
+    const int x = static_cast<int>(blockIdx.x) / per * 8 + sub % 8, mb = sub / 8;
+    if (x >= A.W * C.Hkv) return;
+    const int h = x % C.Hkv, w = x / C.Hkv;
+    long long total, pre;
+    {
+        long long unused;
+        total = units_total(A, plan, 0, unused);
+    }
+    long long at = range_start(A, total, w);
+    const long long end = range_start(A, total, w + 1);
+    if (at >= end) return;
+    int b = units_find(A, plan, at, pre);
+
+    unsigned char* kt = lds + wv * 2 * S::KB;
+    unsigned char* vt = kt + S::KB;
+    const char* kbase = C.k + h * C.ks[1];
+    const char* vbase = C.v + h * C.vs[1];
+    const float ksc = E4M3 ? C.k_scale[h] : 1.0f, vsc = E4M3 ? C.v_scale[h] : 1.0f;
+    const float scale = A.scale * ksc;
+    const int slot_mask = (1 << C.shift) - 1;
+    const int m0 = mb * M16;
+
+    while (at < end) {
+        const Seq s = seq_of(A, b);
+        const int u0 = static_cast<int>(at - pre);
+        const int u1 = static_cast<int>(end - pre < s.units ? end - pre : s.units);
+        at += u1 - u0;
+        if (s.n == 0) {                                    // bad lengths: one unit, NaN
+            for (int i = t; i < M16 * D; i += NTQ) {
+                const int m = m0 + i / D;
+                if (m < A.M) {
+                    const long long row = (static_cast<long long>(b) * C.R + m / A.G) * A.Hq + h * A.G + m % A.G;
+                    reinterpret_cast<typename T::type*>(A.out)[row * D + i % D] = static_cast<typename T::type>(NAN);
+                }
+            }
+            pre += 1;
+            ++b;
+            continue;
+        }
+        const bool whole = u0 == 0 && u1 == s.units;
+        const int beg = s.base + u0 * TU, stop = min(s.hi, s.base + u1 * TU);
+        const int tiles = (stop - beg + TT - 1) / TT;
+        const int* table = C.table + static_cast<long long>(b) * C.max_pages;
+        int bad = 0;
+        // the page of key tile * TT + lane % 32 of the range; keys nobody sees are
+        // taken from the nearest that somebody does (and masked)
+        auto key_of = [&](int tile, int row) { return min(max(beg + tile * TT + row, s.lo), s.hi - 1); };
+        auto page_of = [&](int tile) {
+            int p = table[key_of(tile, lane & (TT - 1)) >> C.shift];
+            if (!page_ok(C, p)) { bad = 1; p = 0; }
+            return p;
+        };
+        auto issue = [&](unsigned char* dst, const char* base, const long long (&str)[3], int tile, int pages) {
+#pragma unroll
+            for (int j = 0; j < S::NL; ++j) {
+                const int row = j * S::RPI + lane / S::CPR;
+                const int page = __shfl(pages, row, 64);
+                const int slot = key_of(tile, row) & slot_mask;
+                const int chunk = (lane % S::CPR) ^ S::swz(row);
+                const char* src = base + page * str[0] + slot * str[2] + chunk * 16;
+                __builtin_amdgcn_global_load_lds((glb_ptr)src, (lds_ptr)(dst + j * 1024), 16, 0, 0);
+            }
+        };
+        int tile = wv;
+        int page1 = 0;
+        if (tile < tiles) {
+            const int page0 = page_of(tile);
+            if (tile + NWQ < tiles) page1 = page_of(tile + NWQ);
+            issue(kt, kbase, C.ks, tile, page0);
+            issue(vt, vbase, C.vs, tile, page0);
+        }
+        // this lane's query rows: the MFMA's B operand, and where each one stands
+        i32x4 qf[MT][NC];
+        int pos[MT];                                       // the row's position
+        float slope[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int m = m0 + mt * 16 + r16;
+            const int i = m < A.M ? m / A.G : 0, hq = h * A.G + (m < A.M ? m % A.G : 0);
+            const char* row = A.q + b * A.qs[0] + i * A.qs[1] + hq * A.qs[2];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                // the products with 8 bits take 16 consecutive elements of a key per lane
+                const int d = E4M3 ? (c / 2) * 64 + g * 16 + (c & 1) * 8 : c * 32 + g * 8;
+                qf[mt][c] = *reinterpret_cast<const i32x4*>(row + d * 2);
+                if (m >= A.M) qf[mt][c] = i32x4{0, 0, 0, 0};
+            }
+            pos[mt] = s.kv + min(i, s.n - 1);
+            slope[mt] = A.slopes ? A.slopes[hq] * LOG2E : 0.0f;
+        }
+        f32x4 acc[ND][MT];
+        float mx[MT], sum[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            mx[mt] = -F32_MAX;
+            sum[mt] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) acc[d][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        for (; tile < tiles; tile += NWQ) {
+            const bool more = tile + NWQ < tiles;
+            const int tok = beg + tile * TT;
+            wait_loads<S::NL>();                           // the keys are in, the values may not be
+            f32x4 sc[2][MT];
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) sc[a][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                const int row = 16 * a + r16;
+                const unsigned char* kr = kt + row * S::RB;
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int c = 0; c < NC; c += 2) {
+                        const i32x4 k16 = *reinterpret_cast<const i32x4*>(kr + (((c / 2) * 4 + g) ^ S::swz(row)) * 16);
+                        const i32x4 k0 = widen8<T>(i32x2{k16.x, k16.y}), k1 = widen8<T>(i32x2{k16.z, k16.w});
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            sc[a][mt] = mfma<T>(k0, qf[mt][c], sc[a][mt]);
+                            sc[a][mt] = mfma<T>(k1, qf[mt][c + 1], sc[a][mt]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        const i32x4 kf = *reinterpret_cast<const i32x4*>(kr + ((c * 4 + g) ^ S::swz(row)) * 16);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) sc[a][mt] = mfma<T>(kf, qf[mt][c], sc[a][mt]);
+                    }
+                }
+            }
+            wait_lds();                                    // the keys' place is free
+            int page2 = 0;
+            if (more) {
+                if (tile + 2 * NWQ < tiles) page2 = page_of(tile + 2 * NWQ);
+                issue(kt, kbase, C.ks, tile + NWQ, page1);
+            }
+            // scores in units of log2, masked
+            const bool edge = tok + TT - 1 > s.kv || (A.window > 0 && tok <= s.hi - 1 - A.window);
+            bool up = false;
+            float top[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                top[mt] = -INFINITY;
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float v = sc[a][mt][r];
+                        if (A.softcap > 0.0f) {            // cap tanh(v / cap) = cap (1 - 2 / (1 + e^(2 v / cap)))
+                            const float e = __builtin_amdgcn_exp2f(v * (scale / A.softcap * 2.0f * LOG2E));
+                            v = A.softcap * LOG2E * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
+                        } else {
+                            v *= scale * LOG2E;
+                        }
+                        const int key = tok + 16 * a + 4 * g + r;
+                        if (A.slopes) v += slope[mt] * static_cast<float>(key - pos[mt]);
+                        if (edge && (key > pos[mt] || (A.window > 0 && key <= pos[mt] - A.window))) v = -INFINITY;
+                        sc[a][mt][r] = v;
+                        top[mt] = fmaxf(top[mt], v);
+                    }
+                up = up || top[mt] > mx[mt] + LAZY;
+            }
+            if (__any(up)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    float n = top[mt];
+                    n = fmaxf(n, __shfl_xor(n, 16, 64));
+                    n = fmaxf(n, __shfl_xor(n, 32, 64));
+                    n = fmaxf(n, mx[mt]);
+                    const float f = __builtin_amdgcn_exp2f(mx[mt] - n);
+                    mx[mt] = n;
+                    sum[mt] *= f;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) acc[d][mt] *= f;
+                }
+            }
+            i32x4 pf[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    float p[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        p[r] = __builtin_amdgcn_exp2f(sc[a][mt][r] - mx[mt]);
+                        sum[mt] += p[r];
+                    }
+                    // rounded once to the operand type of the matrix cores
+                    pf[mt][2 * a] = static_cast<int>(pack2<T>(p[0], p[1]));
+                    pf[mt][2 * a + 1] = static_cast<int>(pack2<T>(p[2], p[3]));
+                }
+            }
+            if (more) wait_loads<S::NL>();                 // the values are in
+            else wait_loads<0>();
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                i32x4 vf;
+                if constexpr (E4M3) {
+                    const int rr = r16 >> 1, row = rr < 4 ? 4 * g + rr : 12 + 4 * g + rr;
+                    vf = widen8<T>(__builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                        (lds_i32x2)(vt + row * S::RB + (d ^ S::swz(row)) * 16 + (r16 & 1) * 8)));
+                } else {
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        const int row = 16 * a + 4 * g + (r16 >> 2), c = 2 * d + ((r16 >> 1) & 1);
+                        const i32x2 v = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (lds_i16x4)(vt + row * S::RB + (c ^ S::swz(row)) * 16 + (r16 & 1) * 8)));
+                        vf[2 * a] = v.x;
+                        vf[2 * a + 1] = v.y;
+                    }
+                }
+                if (!edge) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) acc[d][mt] = mfma<T>(vf, pf[mt], acc[d][mt]);
+                    continue;
+                }
+                // Keys that only some rows see (or none): a weight of zero does not
+                // cancel a value that is not finite, so such values are taken out.
+                bool odd = false;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int key = tok + (j < 4 ? 4 * g + j : 12 + 4 * g + j);
+                    const unsigned half = j & 1 ? 0xffff0000u : 0xffffu;
+                    if (key < s.lo || key >= s.hi) vf[j / 2] = static_cast<int>(static_cast<unsigned>(vf[j / 2]) & ~half);
+                    const unsigned e = T::EXP << (j & 1 ? 16 : 0);
+                    odd = odd || (static_cast<unsigned>(vf[j / 2]) & e) == e;
+                }
+                if (!__any(odd)) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) acc[d][mt] = mfma<T>(vf, pf[mt], acc[d][mt]);
+                    continue;
+                }
+                for (int i = 0; i < s.n; ++i) {            // position by position, without what it does not see
+                    i32x4 vi = vf;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int key = tok + (j < 4 ? 4 * g + j : 12 + 4 * g + j);
+                        const unsigned half = j & 1 ? 0xffff0000u : 0xffffu;
+                        if (key > s.kv + i || (A.window > 0 && key <= s.kv + i - A.window))
+                            vi[j / 2] = static_cast<int>(static_cast<unsigned>(vi[j / 2]) & ~half);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const f32x4 z = mfma<T>(vi, pf[mt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                        if (pos[mt] == s.kv + i) acc[d][mt] += z;
+                    }
+                }
+            }
+            wait_lds();                                    // the values' place is free
+            if (more) issue(vt, vbase, C.vs, tile + NWQ, page1);
+            page1 = page2;
+        }
+        // ---- join the four waves
+        const bool nan = __any(bad);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float l = sum[mt];
+            l += __shfl_xor(l, 16, 64);
+            l += __shfl_xor(l, 32, 64);
+            if (nan) l = NAN;
+            if (g == 0) {
+                st_m[wv][mt * 16 + r16] = mx[mt];
+                st_l[wv][mt * 16 + r16] = l;
+            }
+        }
+        __syncthreads();                                   // the statistics are in, the tiles are free
+        float* slot = A.ws + (static_cast<long long>(w * C.Hkv + h) * A.MB + mb) * (2ll * M16 * (D + 2)) +
+                      (u0 == 0 ? M16 * (D + 2) : 0);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int m = mt * 16 + r16;
+            float n = st_m[0][m];
+#pragma unroll
+            for (int j = 1; j < NWQ; ++j) n = fmaxf(n, st_m[j][m]);
+            float l = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NWQ; ++j) l += st_l[j][m] * __builtin_amdgcn_exp2f(st_m[j][m] - n);
+            const float f = __builtin_amdgcn_exp2f(mx[mt] - n);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) acc[d][mt] *= f;
+            if (t < 16) {                                  // group 0 of wave 0
+                fin[m] = l;
+                if (!whole) {
+                    slot[M16 * D + 2 * m] = n;
+                    slot[M16 * D + 2 * m + 1] = l;
+                }
+            }
+        }
+        constexpr int FIT = S::LDS / (NWQ * M16 * 64);     // 16-element column blocks that fit
+        constexpr int DC = FIT >= ND ? ND : FIT >= 8 ? 8 : FIT >= 4 ? 4 : FIT >= 2 ? 2 : 1;
+        static_assert(FIT >= 1, "exchange");
+        float* ex = reinterpret_cast<float*>(lds);         // [wave][M16][16 DC]
+#pragma unroll
+        for (int d0 = 0; d0 < ND; d0 += DC) {
+#pragma unroll
+            for (int d = 0; d < DC; ++d)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    *reinterpret_cast<f32x4*>(ex + ((wv * M16 + mt * 16 + r16) * DC + d) * 16 + 4 * g) = acc[d0 + d][mt];
+            __syncthreads();
+            for (int i = t; i < M16 * DC * 4; i += NTQ) {
+                const int m = i / (DC * 4), d = d0 * 16 + i % (DC * 4) * 4;
+                if (m0 + m >= A.M) continue;
+                f32x4 o = *reinterpret_cast<const f32x4*>(ex + 4 * i);
+#pragma unroll
+                for (int j = 1; j < NWQ; ++j) o += *reinterpret_cast<const f32x4*>(ex + j * M16 * DC * 16 + 4 * i);
+                if (whole) {
+                    const int tk = (m0 + m) / A.G, hq = h * A.G + (m0 + m) % A.G;
+                    u32x2 y = {0, 0};
+                    if (tk < s.n) {
+                        const float inv = vsc / fin[m];
+                        y.x = pack2<T>(o.x * inv, o.y * inv);
+                        y.y = pack2<T>(o.z * inv, o.w * inv);
+                    }
+                    const long long row = (static_cast<long long>(b) * C.R + tk) * A.Hq + hq;
+                    *reinterpret_cast<u32x2*>(A.out + (row * D + d) * 2) = y;
+                } else {
+                    *reinterpret_cast<f32x4*>(slot + m * D + d) = o;
+                }
+            }
+            __syncthreads();
+        }
+        if (u1 == s.units) { pre += s.units; ++b; }
+    }
+}
+
+// Merges the pieces of a sequence that crosses ranges: one workgroup per cache head,
+// row block, group of query rows and batch row (or, with more batch rows than
+// ranges, border between ranges: the first border inside a sequence stands for it).
+template <class T>
+__global__ __launch_bounds__(NTQ) void join_kernel(AttnParams A) {
+    __shared__ Plan plan;
+    const Cache& C = A.c;
+    const int t = static_cast<int>(threadIdx.x), cols = A.D / 4, rows = NTQ / cols;
+    const int groups = (A.M16 + rows - 1) / rows;
+    int x = static_cast<int>(blockIdx.x);
+    const int gr = x % groups; x /= groups;
+    const int mb = x % A.MB; x /= A.MB;
+    const int h = x % C.Hkv; x /= C.Hkv;
+    int b = x;
+    long long pre;
+    const long long total = units_total(A, plan, b, pre);
+    if (!A.direct) {
+        const long long border = range_start(A, total, x + 1);
+        if (border >= total) return;
+        b = units_find(A, plan, border, pre);
+        if (border == pre || range_start(A, total, x) > pre) return;
+    }
+    const Seq s = seq_of(A, b);
+    const long long fin = pre + s.units;
+    // the first and the last range that hold units of the sequence
+    const int wa = static_cast<int>(((pre + 1) * A.W + total - 1) / total) - 1;
+    const int wb = static_cast<int>((fin * A.W + total - 1) / total) - 1;
+    if (wa >= wb) return;
+    const int m = gr * rows + t / cols, d = t % cols * 4, tk = (mb * A.M16 + m) / A.G;
+    if (m >= A.M16 || mb * A.M16 + m >= A.M) return;
+    const long long size = static_cast<long long>(A.M16) * (A.D + 2);
+    float n = -F32_MAX, l = 0.0f;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int w = wa; w <= wb; ++w) {
+        const long long from = range_start(A, total, w);
+        if (from >= range_start(A, total, w + 1)) continue;
+        const float* slot = A.ws + ((static_cast<long long>(w) * C.Hkv + h) * A.MB + mb) * 2 * size +
+                            (from <= pre ? size : 0);
+        const float pm = slot[A.M16 * A.D + 2 * m], pl = slot[A.M16 * A.D + 2 * m + 1];
+        const f32x4 po = *reinterpret_cast<const f32x4*>(slot + m * A.D + d);
+        const float nn = fmaxf(n, pm), f = __builtin_amdgcn_exp2f(n - nn), pf = __builtin_amdgcn_exp2f(pm - nn);
+        n = nn;
+        l = l * f + pl * pf;
+        o = o * f + po * pf;
+    }
+    u32x2 y = {0, 0};
+    if (tk < s.n) {
+        const float inv = (C.v_scale ? C.v_scale[h] : 1.0f) / l;
+        y.x = pack2<T>(o.x * inv, o.y * inv);
+        y.y = pack2<T>(o.z * inv, o.w * inv);
+    }
+    const long long row = (static_cast<long long>(b) * C.R + tk) * A.Hq + h * A.G + (mb * A.M16 + m) % A.G;
+    *reinterpret_cast<u32x2*>(A.out + (row * A.D + d) * 2) = y;
 }
 
 // ------------------------------------------------------------------ logit adjustment
@@ -508,17 +1037,69 @@ int check_cache(int dtype, int32_t B, int32_t R, int32_t max_R, int32_t Hkv, int
     return SPEC_OK;
 }
 
+// Row blocks, ranges and workspace of an attention call.
+struct AttnPlan {
+    int M, MB, MT, W;
+    size_t bytes;
+};
+
+int attn_occupancy_of(int D, int MT, bool e4m3) {
+#define SPEC_OCC(d) (e4m3 ? MT == 1 ? attn_occupancy<d, 1, true>() : MT == 2 ? attn_occupancy<d, 2, true>() :         \
+                     MT == 3 ? attn_occupancy<d, 3, true>() : attn_occupancy<d, 4, true>() :                          \
+                     MT == 1 ? attn_occupancy<d, 1, false>() : MT == 2 ? attn_occupancy<d, 2, false>() :              \
+                     MT == 3 ? attn_occupancy<d, 3, false>() : attn_occupancy<d, 4, false>())
+    return D == 64 ? SPEC_OCC(64) : D == 128 ? SPEC_OCC(128) : SPEC_OCC(256);
+#undef SPEC_OCC
+}
+
+AttnPlan attn_plan(int B, int R, int Hq, int Hkv, int D, bool e4m3, int page_size, int max_pages) {
+    AttnPlan p;
+    p.M = R * (Hq / Hkv);
+    const int tiles = (p.M + 15) / 16, most = D == 256 ? 2 : 4;
+    p.MB = (tiles + most - 1) / most;
+    p.MT = (tiles + p.MB - 1) / p.MB;
+    // one resident round, but no more ranges than there can be units
+    const int lanes = Hkv * p.MB;
+    long long w = CUS * attn_occupancy_of(D, p.MT, e4m3) / lanes;
+    const long long units = B * ((static_cast<long long>(max_pages) * page_size + TT + TU - 1) / TU);
+    if (w > units) w = units;
+    p.W = w < 1 ? 1 : static_cast<int>(w);
+    p.bytes = static_cast<size_t>(lanes) * p.W * 2 * 16 * p.MT * (D + 2) * sizeof(float);
+    p.bytes = p.W == 1 ? 256 : (p.bytes + 255) & ~static_cast<size_t>(255);
+    return p;
+}
+
+template <class T, int D, bool E4M3>
+void launch_attn_m(const AttnParams& A, int MT, unsigned grid, hipStream_t s) {
+    if (MT == 1) hipLaunchKernelGGL((attn_kernel<T, D, 1, E4M3>), dim3(grid), dim3(NTQ), 0, s, A);
+    else if (MT == 2) hipLaunchKernelGGL((attn_kernel<T, D, 2, E4M3>), dim3(grid), dim3(NTQ), 0, s, A);
+    if constexpr (D < 256) {
+        if (MT == 3) hipLaunchKernelGGL((attn_kernel<T, D, 3, E4M3>), dim3(grid), dim3(NTQ), 0, s, A);
+        else if (MT == 4) hipLaunchKernelGGL((attn_kernel<T, D, 4, E4M3>), dim3(grid), dim3(NTQ), 0, s, A);
+    }
+}
+
 template <class T, int D>
-void launch_attn_d(const AttnParams& A, bool e4m3, unsigned grid, hipStream_t s) {
-    if (e4m3) hipLaunchKernelGGL((attn_kernel<T, D, true>), dim3(grid), dim3(NTQ), 0, s, A);
-    else hipLaunchKernelGGL((attn_kernel<T, D, false>), dim3(grid), dim3(NTQ), 0, s, A);
+void launch_attn_d(const AttnParams& A, int MT, bool e4m3, unsigned grid, hipStream_t s) {
+    if (e4m3) launch_attn_m<T, D, true>(A, MT, grid, s);
+    else launch_attn_m<T, D, false>(A, MT, grid, s);
 }
 
 template <class T>
-void launch_attn(const AttnParams& A, int D, bool e4m3, unsigned grid, hipStream_t s) {
-    if (D == 64) launch_attn_d<T, 64>(A, e4m3, grid, s);
-    else if (D == 128) launch_attn_d<T, 128>(A, e4m3, grid, s);
-    else launch_attn_d<T, 256>(A, e4m3, grid, s);
+int launch_attn(AttnParams& A, int MT, bool e4m3, hipStream_t s) {
+    const long long x = static_cast<long long>(A.W) * A.c.Hkv;
+    const long long grid = (x + 7) / 8 * 8 * A.MB;
+    if (grid > (1ll << 31) - 1) return fail(SPEC_ERR_SHAPE, "R * Hq is too large");
+    if (A.D == 64) launch_attn_d<T, 64>(A, MT, e4m3, static_cast<unsigned>(grid), s);
+    else if (A.D == 128) launch_attn_d<T, 128>(A, MT, e4m3, static_cast<unsigned>(grid), s);
+    else launch_attn_d<T, 256>(A, MT, e4m3, static_cast<unsigned>(grid), s);
+    const int rc = launched();
+    if (rc != SPEC_OK || A.W == 1) return rc;              // one range: nothing crosses
+    A.direct = A.c.B < A.W;
+    const int rows = NTQ / (A.D / 4), groups = (A.M16 + rows - 1) / rows;
+    const long long join = static_cast<long long>(A.direct ? A.c.B : A.W - 1) * A.c.Hkv * A.MB * groups;
+    hipLaunchKernelGGL((join_kernel<T>), dim3(static_cast<unsigned>(join)), dim3(NTQ), 0, s, A);
+    return launched();
 }
 
 }  // namespace
@@ -565,7 +1146,7 @@ size_t spec_attention_workspace_size(int32_t B, int32_t R, int32_t Hq, int32_t H
         max_pages < 1 || (cache_dtype != SPEC_DTYPE_BF16 && cache_dtype != SPEC_DTYPE_F16 &&
                           cache_dtype != SPEC_DTYPE_E4M3))
         return 0;
-    return 256;
+    return attn_plan(B, R, Hq, Hkv, D, cache_dtype == SPEC_DTYPE_E4M3, page_size, max_pages).bytes;
 }
 
 int spec_attention(const void* q, const int64_t* q_stride, int dtype, int32_t B, int32_t R, int32_t Hq, int32_t Hkv,
@@ -588,23 +1169,21 @@ int spec_attention(const void* q, const int64_t* q_stride, int dtype, int32_t B,
     if (!aligned(q, 16) || !strides_ok(q_stride, 2, A.qs) || !aligned(out, 16))
         return fail(SPEC_ERR_ALIGN, "q and out must be 16-byte aligned and q's strides multiples of 8 elements");
     if (slopes && !aligned(slopes, 4)) return fail(SPEC_ERR_ALIGN, "slopes is not aligned to its element size");
-    const size_t need = spec_attention_workspace_size(B, R, Hq, Hkv, D, cache_dtype, page_size, max_pages);
-    if (!workspace || workspace_bytes < need)
-        return fail(SPEC_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu%s)", need, workspace_bytes,
+    const bool e4m3 = cache_dtype == SPEC_DTYPE_E4M3;
+    const AttnPlan plan = attn_plan(B, R, Hq, Hkv, D, e4m3, page_size, max_pages);
+    if (!workspace || workspace_bytes < plan.bytes)
+        return fail(SPEC_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu%s)", plan.bytes, workspace_bytes,
                     workspace ? "" : ", NULL");
     if (!aligned(workspace, 256)) return fail(SPEC_ERR_ALIGN, "workspace must be 256-byte aligned");
     A.q = static_cast<const char*>(q);
     A.slopes = slopes;
     A.out = static_cast<char*>(out);
+    A.ws = static_cast<float*>(workspace);
     A.scale = scale; A.softcap = softcap; A.window = window;
-    A.Hq = Hq; A.G = Hq / Hkv;
-    const long long grid = static_cast<long long>(B) * R * Hq;
-    if (grid > (1ll << 31) - 1) return fail(SPEC_ERR_SHAPE, "B * R * Hq exceeds 2^31 - 1");
-    const bool e4m3 = cache_dtype == SPEC_DTYPE_E4M3;
+    A.Hq = Hq; A.G = Hq / Hkv; A.D = D;
+    A.M = plan.M; A.MB = plan.MB; A.M16 = 16 * plan.MT; A.W = plan.W;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (dtype == SPEC_DTYPE_BF16) launch_attn<Bf16>(A, D, e4m3, static_cast<unsigned>(grid), s);
-    else launch_attn<F16>(A, D, e4m3, static_cast<unsigned>(grid), s);
-    return launched();
+    return dtype == SPEC_DTYPE_BF16 ? launch_attn<Bf16>(A, plan.MT, e4m3, s) : launch_attn<F16>(A, plan.MT, e4m3, s);
 }
 
 int spec_adjust(const void* logits, int32_t B, int32_t R, int32_t V, int dtype, const int32_t* draft_tokens, int32_t k,
