@@ -55,6 +55,7 @@ inline emu_f16x2 emu_cvt_f16_fp8(int w, float, bool hi) {
     return emu_f16x2{static_cast<_Float16>(emu_e4m3_value(p & 255)), static_cast<_Float16>(emu_e4m3_value((p >> 8) & 255))};
 }
 #define __builtin_amdgcn_cvt_scalef32_pk_f16_fp8 emu_cvt_f16_fp8
+#define __builtin_amdgcn_readlane(v, l) __shfl((v), (l), 64)
 inline float emu_rcpf(float x) { return 1.0f / x; }
 #define __builtin_amdgcn_rcpf emu_rcpf
 

@@ -237,6 +237,18 @@ __device__ inline Seq seq_of(const AttnParams& A, int b) {
     return s;
 }
 
+template <bool B>
+struct Bool {
+    static constexpr bool value = B;
+};
+
+// x, which the compiler must not know: keeps the addresses that derive from it from being
+// computed before a loop and held in registers (dozens of them) throughout
+__device__ inline int opaque(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 struct Plan {
     long long wave[NWQ];
     long long total, pre;
@@ -348,11 +360,40 @@ __device__ inline i32x4 widen8(i32x2 w) {
     return o;
 }
 
+// Makes zeros of the values in these 16 bytes that are NaN or infinite; whether there were any.
+template <class T, bool E4M3>
+__device__ inline bool strip(i32x4& w) {
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        unsigned u = static_cast<unsigned>(w[j]);
+#pragma unroll
+        for (int q = 0; q < (E4M3 ? 4 : 2); ++q) {
+            const unsigned e = E4M3 ? 0x7fu << (8 * q) : T::EXP << (16 * q), all = E4M3 ? 0xffu << (8 * q) : 0xffffu << (16 * q);
+            if ((u & e) == e) { odd = true; u &= ~all; }
+        }
+        w[j] = static_cast<int>(u);
+    }
+    return odd;
+}
+
+// element d of a value in the cache
+template <class T, bool E4M3>
+__device__ inline float value_at(const char* row, int d) {
+    if constexpr (E4M3) {
+        const i32x4 w = widen8<T>(i32x2{static_cast<int>(reinterpret_cast<const unsigned char*>(row)[d]), 0});
+        return T::lo(static_cast<unsigned>(w.x));
+    } else {
+        return T::lo(reinterpret_cast<const unsigned short*>(row)[d]);
+    }
+}
+
 template <int D, bool E4M3>
 struct TileShape {
     static constexpr int RB = D * (E4M3 ? 1 : 2);          // bytes of a row (one key or value)
     static constexpr int CPR = RB / 16;                    // 16-byte chunks of a row
     static constexpr int RPI = 64 / CPR;                   // rows one load instruction of a wave fills
+    static constexpr int RPI_SHIFT = RPI == 16 ? 4 : RPI == 8 ? 3 : RPI == 4 ? 2 : 1;
     static constexpr int NL = TT / RPI;                    // load instructions per tile
     static constexpr int KB = TT * RB;                     // bytes of a tile
     static constexpr int LDS = NWQ * 2 * KB;
@@ -363,21 +404,24 @@ struct TileShape {
     }
 };
 
-// workgroups per CU: as many as LDS and about 512 / 4 .. 512 registers per lane allow
+// Workgroups per CU (waves per SIMD): as many as LDS and the registers allow: the
+// accumulators, the queries, scores and weights, and about 70 for the rest.
 template <int D, int MT, bool E4M3>
 constexpr int attn_occupancy() {
     constexpr int lds = 160 * 1024 / (TileShape<D, E4M3>::LDS + 3 * 1024);
-    constexpr int regs = MT * D <= 128 ? 4 : MT * D <= 192 ? 3 : MT * D <= 512 ? 2 : 1;
-    return lds < regs ? lds : regs;
+    constexpr int regs = 512 / (D * MT / 4 + D * MT / 8 + 12 * MT + 70);
+    return lds < regs ? lds : regs < 4 ? regs : 4;
 }
 
 template <class T, int D, int MT, bool E4M3>
 __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_kernel(AttnParams A) {
     using S = TileShape<D, E4M3>;
     constexpr int M16 = 16 * MT, ND = D / 16, NC = D / 32;
-    __shared__ __attribute__((aligned(16))) unsigned char lds[S::LDS];
+    // two arrays, so that the compiler knows that a load into one does not write the other
+    __shared__ __attribute__((aligned(16))) unsigned char lds_k[NWQ * S::KB], lds_v[NWQ * S::KB];
     __shared__ float st_m[NWQ][M16], st_l[NWQ][M16], fin[M16];
     __shared__ Plan plan;
+    __shared__ int odd_any;                                // some edge value was not finite
     const Cache& C = A.c;
     const int t = static_cast<int>(threadIdx.x), lane = t & 63, wv = __builtin_amdgcn_readfirstlane(t >> 6);
     const int r16 = lane & 15, g = lane >> 4;
@@ -396,8 +440,11 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
     if (at >= end) return;
     int b = units_find(A, plan, at, pre);
 
-    unsigned char* kt = lds + wv * 2 * S::KB;
-    unsigned char* vt = kt + S::KB;
+    if (t == 0) odd_any = 0;
+    __syncthreads();
+
+    unsigned char* kt = lds_k + wv * S::KB;
+    unsigned char* vt = lds_v + wv * S::KB;
     const char* kbase = C.k + h * C.ks[1];
     const char* vbase = C.v + h * C.vs[1];
     const float ksc = E4M3 ? C.k_scale[h] : 1.0f, vsc = E4M3 ? C.v_scale[h] : 1.0f;
@@ -406,11 +453,15 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
     const int m0 = mb * M16;
 
     while (at < end) {
-        const Seq s = seq_of(A, b);
-        const int u0 = static_cast<int>(at - pre);
-        const int u1 = static_cast<int>(end - pre < s.units ? end - pre : s.units);
+        const Seq sq = seq_of(A, b);
+        // the same in every lane: scalars
+        const int kv = __builtin_amdgcn_readfirstlane(sq.kv), n_tok = __builtin_amdgcn_readfirstlane(sq.n);
+        const int lo = __builtin_amdgcn_readfirstlane(sq.lo), hi = __builtin_amdgcn_readfirstlane(sq.hi);
+        const int base = __builtin_amdgcn_readfirstlane(sq.base), units = __builtin_amdgcn_readfirstlane(sq.units);
+        const int u0 = __builtin_amdgcn_readfirstlane(static_cast<int>(at - pre));
+        const int u1 = __builtin_amdgcn_readfirstlane(static_cast<int>(end - pre < units ? end - pre : units));
         at += u1 - u0;
-        if (s.n == 0) {                                    // bad lengths: one unit, NaN
+        if (n_tok == 0) {                                  // bad lengths: one unit, NaN
             for (int i = t; i < M16 * D; i += NTQ) {
                 const int m = m0 + i / D;
                 if (m < A.M) {
@@ -422,35 +473,51 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
             ++b;
             continue;
         }
-        const bool whole = u0 == 0 && u1 == s.units;
-        const int beg = s.base + u0 * TU, stop = min(s.hi, s.base + u1 * TU);
+        const bool whole = u0 == 0 && u1 == units;
+        const int beg = base + u0 * TU, stop = min(hi, base + u1 * TU);
         const int tiles = (stop - beg + TT - 1) / TT;
         const int* table = C.table + static_cast<long long>(b) * C.max_pages;
         int bad = 0;
         // the page of key tile * TT + lane % 32 of the range; keys nobody sees are
         // taken from the nearest that somebody does (and masked)
-        auto key_of = [&](int tile, int row) { return min(max(beg + tile * TT + row, s.lo), s.hi - 1); };
+        auto key_of = [&](int tile, int row) { return min(max(beg + tile * TT + row, lo), hi - 1); };
         auto page_of = [&](int tile) {
             int p = table[key_of(tile, lane & (TT - 1)) >> C.shift];
             if (!page_ok(C, p)) { bad = 1; p = 0; }
             return p;
         };
-        auto issue = [&](unsigned char* dst, const char* base, const long long (&str)[3], int tile, int pages) {
+        // A load instruction fills RPI consecutive, aligned rows. They lie in one page
+        // unless pages are shorter, so page and place are scalars; rows of keys nobody
+        // sees then stand in a page that somebody needs.
+        auto issue = [&](unsigned char* dst, const char* cache, const long long (&str)[3], int tile, int pages) {
+            if (C.shift >= S::RPI_SHIFT) {
+                const int lrow = opaque(lane / S::CPR);
+                const unsigned row_off = static_cast<unsigned>(lrow) * static_cast<unsigned>(str[2]);
 #pragma unroll
-            for (int j = 0; j < S::NL; ++j) {
-                const int row = j * S::RPI + lane / S::CPR;
-                const int page = __shfl(pages, row, 64);
-                const int slot = key_of(tile, row) & slot_mask;
-                const int chunk = (lane % S::CPR) ^ S::swz(row);
-                const char* src = base + page * str[0] + slot * str[2] + chunk * 16;
-                __builtin_amdgcn_global_load_lds((glb_ptr)src, (lds_ptr)(dst + j * 1024), 16, 0, 0);
+                for (int j = 0; j < S::NL; ++j) {
+                    const int page = __builtin_amdgcn_readlane(pages, j * S::RPI);
+                    const int slot = (beg + tile * TT + j * S::RPI) & slot_mask;
+                    const char* src = cache + page * str[0] + slot * str[2];
+                    const unsigned off = row_off + static_cast<unsigned>((lane % S::CPR) ^ S::swz(j * S::RPI + lrow)) * 16u;
+                    __builtin_amdgcn_global_load_lds((glb_ptr)(src + off), (lds_ptr)(dst + j * 1024), 16, 0, 0);
+                }
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < S::NL; ++j) {
+                    const int row = j * S::RPI + lane / S::CPR;
+                    const int page = __shfl(pages, row, 64);
+                    const int slot = key_of(tile, row) & slot_mask;
+                    const int chunk = (lane % S::CPR) ^ S::swz(row);
+                    const char* src = cache + page * str[0] + slot * str[2] + chunk * 16;
+                    __builtin_amdgcn_global_load_lds((glb_ptr)src, (lds_ptr)(dst + j * 1024), 16, 0, 0);
+                }
             }
         };
         int tile = wv;
         int page1 = 0;
         if (tile < tiles) {
             const int page0 = page_of(tile);
-            if (tile + NWQ < tiles) page1 = page_of(tile + NWQ);
+            page1 = page_of(tile + NWQ);
             issue(kt, kbase, C.ks, tile, page0);
             issue(vt, vbase, C.vs, tile, page0);
         }
@@ -470,7 +537,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                 qf[mt][c] = *reinterpret_cast<const i32x4*>(row + d * 2);
                 if (m >= A.M) qf[mt][c] = i32x4{0, 0, 0, 0};
             }
-            pos[mt] = s.kv + min(i, s.n - 1);
+            pos[mt] = kv + min(i, n_tok - 1);
             slope[mt] = A.slopes ? A.slopes[hq] * LOG2E : 0.0f;
         }
         f32x4 acc[ND][MT];
@@ -482,21 +549,22 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
 #pragma unroll
             for (int d = 0; d < ND; ++d) acc[d][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        for (; tile < tiles; tile += NWQ) {
-            const bool more = tile + NWQ < tiles;
-            const int tok = beg + tile * TT;
+        // one tile; MORE: the wave has another, whose loads are issued as places get free
+        auto step = [&](auto MORE) {
+            constexpr bool more = decltype(MORE)::value;
+            const int tok = beg + tile * TT, ro = opaque(r16), go = opaque(g);
             wait_loads<S::NL>();                           // the keys are in, the values may not be
             f32x4 sc[2][MT];
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) sc[a][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                const int row = 16 * a + r16;
+                const int row = 16 * a + ro;
                 const unsigned char* kr = kt + row * S::RB;
                 if constexpr (E4M3) {
 #pragma unroll
                     for (int c = 0; c < NC; c += 2) {
-                        const i32x4 k16 = *reinterpret_cast<const i32x4*>(kr + (((c / 2) * 4 + g) ^ S::swz(row)) * 16);
+                        const i32x4 k16 = *reinterpret_cast<const i32x4*>(kr + (((c / 2) * 4 + go) ^ S::swz(row)) * 16);
                         const i32x4 k0 = widen8<T>(i32x2{k16.x, k16.y}), k1 = widen8<T>(i32x2{k16.z, k16.w});
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
@@ -507,7 +575,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                 } else {
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        const i32x4 kf = *reinterpret_cast<const i32x4*>(kr + ((c * 4 + g) ^ S::swz(row)) * 16);
+                        const i32x4 kf = *reinterpret_cast<const i32x4*>(kr + ((c * 4 + go) ^ S::swz(row)) * 16);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) sc[a][mt] = mfma<T>(kf, qf[mt][c], sc[a][mt]);
                     }
@@ -515,34 +583,54 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
             }
             wait_lds();                                    // the keys' place is free
             int page2 = 0;
-            if (more) {
-                if (tile + 2 * NWQ < tiles) page2 = page_of(tile + 2 * NWQ);
+            if constexpr (more) {
+                page2 = page_of(tile + 2 * NWQ);           // (past the last tile: the last key's)
                 issue(kt, kbase, C.ks, tile + NWQ, page1);
             }
             // scores in units of log2, masked
-            const bool edge = tok + TT - 1 > s.kv || (A.window > 0 && tok <= s.hi - 1 - A.window);
+            const bool edge = tok + TT - 1 > kv || (A.window > 0 && tok <= hi - 1 - A.window);
+            if (A.softcap > 0.0f) {                        // cap tanh(v / cap) = cap (1 - 2 / (1 + e^(2 v / cap)))
+                const float c = A.softcap * LOG2E, e2 = scale / A.softcap * 2.0f * LOG2E;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float e = __builtin_amdgcn_exp2f(sc[j / 4][mt][j % 4] * e2);
+                        sc[j / 4][mt][j % 4] = c - 2.0f * c * __builtin_amdgcn_rcpf(1.0f + e);
+                    }
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sc[j / 4][mt][j % 4] *= scale * LOG2E;
+            }
+            if (A.slopes) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const int away = tok + 4 * g - pos[mt];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        sc[j / 4][mt][j % 4] += slope[mt] * static_cast<float>(away + 16 * (j / 4) + j % 4);
+                }
+            }
+            if (edge) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const int away = tok + 4 * g - pos[mt];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int k = away + 16 * (j / 4) + j % 4;
+                        if (k > 0 || (A.window > 0 && k <= -A.window)) sc[j / 4][mt][j % 4] = -INFINITY;
+                    }
+                }
+            }
             bool up = false;
             float top[MT];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-                top[mt] = -INFINITY;
+                top[mt] = fmaxf(sc[0][mt][0], sc[0][mt][1]);
 #pragma unroll
-                for (int a = 0; a < 2; ++a)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float v = sc[a][mt][r];
-                        if (A.softcap > 0.0f) {            // cap tanh(v / cap) = cap (1 - 2 / (1 + e^(2 v / cap)))
-                            const float e = __builtin_amdgcn_exp2f(v * (scale / A.softcap * 2.0f * LOG2E));
-                            v = A.softcap * LOG2E * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e));
-                        } else {
-                            v *= scale * LOG2E;
-                        }
-                        const int key = tok + 16 * a + 4 * g + r;
-                        if (A.slopes) v += slope[mt] * static_cast<float>(key - pos[mt]);
-                        if (edge && (key > pos[mt] || (A.window > 0 && key <= pos[mt] - A.window))) v = -INFINITY;
-                        sc[a][mt][r] = v;
-                        top[mt] = fmaxf(top[mt], v);
-                    }
+                for (int j = 2; j < 8; ++j) top[mt] = fmaxf(top[mt], sc[j / 4][mt][j % 4]);
                 up = up || top[mt] > mx[mt] + LAZY;
             }
             if (__any(up)) {
@@ -575,65 +663,58 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                     pf[mt][2 * a + 1] = static_cast<int>(pack2<T>(p[2], p[3]));
                 }
             }
-            if (more) wait_loads<S::NL>();                 // the values are in
-            else wait_loads<0>();
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
+            wait_loads<more ? S::NL : 0>();                // the values are in
+            // columns 16 d .. 16 d + 15 of the values as the MFMA's A operand
+            auto value = [&](int d) {
                 i32x4 vf;
                 if constexpr (E4M3) {
-                    const int rr = r16 >> 1, row = rr < 4 ? 4 * g + rr : 12 + 4 * g + rr;
+                    const int rr = ro >> 1, row = rr < 4 ? 4 * go + rr : 12 + 4 * go + rr;
                     vf = widen8<T>(__builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                        (lds_i32x2)(vt + row * S::RB + (d ^ S::swz(row)) * 16 + (r16 & 1) * 8)));
+                        (lds_i32x2)(vt + row * S::RB + (d ^ S::swz(row)) * 16 + (ro & 1) * 8)));
                 } else {
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
-                        const int row = 16 * a + 4 * g + (r16 >> 2), c = 2 * d + ((r16 >> 1) & 1);
+                        const int row = 16 * a + 4 * go + (ro >> 2), c = 2 * d + ((ro >> 1) & 1);
                         const i32x2 v = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (lds_i16x4)(vt + row * S::RB + (c ^ S::swz(row)) * 16 + (r16 & 1) * 8)));
+                            (lds_i16x4)(vt + row * S::RB + (c ^ S::swz(row)) * 16 + (ro & 1) * 8)));
                         vf[2 * a] = v.x;
                         vf[2 * a + 1] = v.y;
                     }
                 }
-                if (!edge) {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) acc[d][mt] = mfma<T>(vf, pf[mt], acc[d][mt]);
-                    continue;
-                }
-                // Keys that only some rows see (or none): a weight of zero does not
-                // cancel a value that is not finite, so such values are taken out.
-                bool odd = false;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int key = tok + (j < 4 ? 4 * g + j : 12 + 4 * g + j);
-                    const unsigned half = j & 1 ? 0xffff0000u : 0xffffu;
-                    if (key < s.lo || key >= s.hi) vf[j / 2] = static_cast<int>(static_cast<unsigned>(vf[j / 2]) & ~half);
-                    const unsigned e = T::EXP << (j & 1 ? 16 : 0);
-                    odd = odd || (static_cast<unsigned>(vf[j / 2]) & e) == e;
-                }
-                if (!__any(odd)) {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) acc[d][mt] = mfma<T>(vf, pf[mt], acc[d][mt]);
-                    continue;
-                }
-                for (int i = 0; i < s.n; ++i) {            // position by position, without what it does not see
-                    i32x4 vi = vf;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int key = tok + (j < 4 ? 4 * g + j : 12 + 4 * g + j);
-                        const unsigned half = j & 1 ? 0xffff0000u : 0xffffu;
-                        if (key > s.kv + i || (A.window > 0 && key <= s.kv + i - A.window))
-                            vi[j / 2] = static_cast<int>(static_cast<unsigned>(vi[j / 2]) & ~half);
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const f32x4 z = mfma<T>(vi, pf[mt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-                        if (pos[mt] == s.kv + i) acc[d][mt] += z;
+                return vf;
+            };
+            if (edge) {
+                // A weight of zero does not cancel a value that is not finite. Values that
+                // nobody sees become zeros; of those that only some rows see what is not
+                // finite does, and is added to the rows that see it at the end.
+                for (int c = lane; c < TT * S::CPR; c += 64) {
+                    i32x4* at16 = reinterpret_cast<i32x4*>(vt + c * 16);
+                    const int key = tok + c / S::CPR;
+                    if (key < lo || key >= hi) {
+                        *at16 = i32x4{0, 0, 0, 0};
+                    } else if (key > kv || (A.window > 0 && key <= hi - 1 - A.window)) {
+                        i32x4 v = *at16;
+                        if (strip<T, E4M3>(v)) { *at16 = v; odd_any = 1; }
                     }
                 }
+                wait_lds();
+            }
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const i32x4 vf = value(d);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) acc[d][mt] = mfma<T>(vf, pf[mt], acc[d][mt]);
             }
             wait_lds();                                    // the values' place is free
-            if (more) issue(vt, vbase, C.vs, tile + NWQ, page1);
-            page1 = page2;
+            if constexpr (more) {
+                issue(vt, vbase, C.vs, tile + NWQ, page1);
+                page1 = page2;
+                tile += NWQ;
+            }
+        };
+        if (tile < tiles) {
+            while (tile + NWQ < tiles) step(Bool<true>());
+            step(Bool<false>());
         }
         // ---- join the four waves
         const bool nan = __any(bad);
@@ -649,6 +730,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
             }
         }
         __syncthreads();                                   // the statistics are in, the tiles are free
+        const bool odd = odd_any != 0;
         float* slot = A.ws + (static_cast<long long>(w * C.Hkv + h) * A.MB + mb) * (2ll * M16 * (D + 2)) +
                       (u0 == 0 ? M16 * (D + 2) : 0);
 #pragma unroll
@@ -671,28 +753,55 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                 }
             }
         }
-        constexpr int FIT = S::LDS / (NWQ * M16 * 64);     // 16-element column blocks that fit
+        // waves 0 and 1 exchange in the keys' array, 2 and 3 in the values': [2][M16][16 DC] each
+        constexpr int FIT = S::KB * NWQ / (2 * M16 * 64);  // 16-element column blocks that fit
         constexpr int DC = FIT >= ND ? ND : FIT >= 8 ? 8 : FIT >= 4 ? 4 : FIT >= 2 ? 2 : 1;
-        static_assert(FIT >= 1, "exchange");
-        float* ex = reinterpret_cast<float*>(lds);         // [wave][M16][16 DC]
+        static_assert(FIT >= 1 && NWQ == 4, "exchange");
+        float* ex0 = reinterpret_cast<float*>(lds_k);
+        float* ex1 = reinterpret_cast<float*>(lds_v);
 #pragma unroll
         for (int d0 = 0; d0 < ND; d0 += DC) {
 #pragma unroll
             for (int d = 0; d < DC; ++d)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    *reinterpret_cast<f32x4*>(ex + ((wv * M16 + mt * 16 + r16) * DC + d) * 16 + 4 * g) = acc[d0 + d][mt];
+                for (int mt = 0; mt < MT; ++mt) {
+                    float* ex = wv < 2 ? ex0 : ex1;
+                    *reinterpret_cast<f32x4*>(ex + (((wv & 1) * M16 + mt * 16 + r16) * DC + d) * 16 + 4 * g) =
+                        acc[d0 + d][mt];
+                }
             __syncthreads();
+            if (t == 0) odd_any = 0;                       // (everyone has read it)
             for (int i = t; i < M16 * DC * 4; i += NTQ) {
                 const int m = i / (DC * 4), d = d0 * 16 + i % (DC * 4) * 4;
                 if (m0 + m >= A.M) continue;
-                f32x4 o = *reinterpret_cast<const f32x4*>(ex + 4 * i);
+                const int half = M16 * DC * 16;
+                f32x4 o = (*reinterpret_cast<const f32x4*>(ex0 + 4 * i) +
+                           *reinterpret_cast<const f32x4*>(ex0 + half + 4 * i)) +
+                          (*reinterpret_cast<const f32x4*>(ex1 + 4 * i) +
+                           *reinterpret_cast<const f32x4*>(ex1 + half + 4 * i));
+                if (odd) {
+                    const int at_pos = kv + min((m0 + m) / A.G, n_tok - 1);
+                    const int from = max(beg, lo), past = min(stop, hi), seen_by_all = hi - A.window;
+                    for (int key = from; key < past; ++key) {
+                        if (key <= kv && (A.window <= 0 || key >= seen_by_all)) {
+                            key = kv;                      // on to those after the first position
+                            continue;
+                        }
+                        if (key > at_pos || (A.window > 0 && key <= at_pos - A.window)) continue;
+                        const int page = table[key >> C.shift];
+                        if (!page_ok(C, page)) continue;
+                        const char* row = vbase + page * C.vs[0] + (key & slot_mask) * C.vs[2];
 #pragma unroll
-                for (int j = 1; j < NWQ; ++j) o += *reinterpret_cast<const f32x4*>(ex + j * M16 * DC * 16 + 4 * i);
+                        for (int j = 0; j < 4; ++j) {
+                            const float v = value_at<T, E4M3>(row, d + j);
+                            if (!(fabsf(v) <= F32_MAX)) o[j] += v;
+                        }
+                    }
+                }
                 if (whole) {
                     const int tk = (m0 + m) / A.G, hq = h * A.G + (m0 + m) % A.G;
                     u32x2 y = {0, 0};
-                    if (tk < s.n) {
+                    if (tk < n_tok) {
                         const float inv = vsc / fin[m];
                         y.x = pack2<T>(o.x * inv, o.y * inv);
                         y.y = pack2<T>(o.z * inv, o.w * inv);
@@ -705,7 +814,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
             }
             __syncthreads();
         }
-        if (u1 == s.units) { pre += s.units; ++b; }
+        if (u1 == units) { pre += units; ++b; }
     }
 }
 
@@ -1027,6 +1136,8 @@ int check_cache(int dtype, int32_t B, int32_t R, int32_t max_R, int32_t Hkv, int
     if (!aligned(table, 4) || !aligned(kv_len, 4) || (draft_len && !aligned(draft_len, 4)) ||
         (k_scale && (!aligned(k_scale, 4) || !aligned(v_scale, 4))))
         return fail(SPEC_ERR_ALIGN, "a tensor pointer is not aligned to its element size");
+    if (C.ks[2] > (1 << 27) || C.vs[2] > (1 << 27))
+        return fail(SPEC_ERR_SHAPE, "a cache's tokens are more than 2^27 bytes apart");
     C.k = const_cast<char*>(static_cast<const char*>(k_cache));
     C.v = const_cast<char*>(static_cast<const char*>(v_cache));
     C.table = table; C.kv_len = kv_len; C.draft_len = draft_len;
