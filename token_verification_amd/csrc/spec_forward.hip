@@ -209,14 +209,16 @@ struct AttnParams {
     long long qs[3];           // bytes between batch rows, tokens, heads
     const float* slopes;       // [Hq] or null
     char* out;                 // [B, R, Hq, D]
-    float* ws;                 // per (w, lane): two slots of M16 * (D + 2) floats
+    float* ws;                 // a Ranges, W RangeRec, then per (w, head, block): two slots of M16 * (D + 2) floats
+    long long slots_at;        // floats before the slots
     float scale, softcap;
     int window, Hq, G, D;
     int M;                     // R * G query rows per cache head
     int MB;                    // row blocks of M16 = 16 * MT rows
     int M16;
     int W;                     // workgroups per cache head and row block
-    int direct;                // join_kernel: one workgroup per batch row (else per range border)
+    int direct;                // join_kernel goes by batch row (else by border between ranges)
+    int slices;                // join_kernel: threads that share a sequence's pieces
 };
 
 // a batch row's keys: positions [lo, hi) are seen by some token in use
@@ -237,9 +239,9 @@ __device__ inline Seq seq_of(const AttnParams& A, int b) {
     return s;
 }
 
-template <bool B>
-struct Bool {
-    static constexpr bool value = B;
+template <int N>
+struct Int {
+    static constexpr int value = N;
 };
 
 // x, which the compiler must not know: keeps the addresses that derive from it from being
@@ -251,7 +253,7 @@ __device__ inline int opaque(int x) {
 
 struct Plan {
     long long wave[NWQ];
-    long long total, pre;
+    long long pre;
     int b;
 };
 
@@ -265,10 +267,11 @@ __device__ inline long long wave_inclusive(long long v) {
     return v;
 }
 
-// Inclusive scan over the workgroup of v; total is its sum. Ends with a barrier.
+// Inclusive scan over the workgroup of v; total is its sum.
 __device__ inline long long block_inclusive(Plan& P, long long v, long long& total) {
     const int w = threadIdx.x >> 6;
     const long long x = wave_inclusive(v);
+    __syncthreads();                                       // the last scan's sums have been read
     if ((threadIdx.x & 63) == 63) P.wave[w] = x;
     __syncthreads();
     long long before = 0;
@@ -278,45 +281,65 @@ __device__ inline long long block_inclusive(Plan& P, long long v, long long& tot
         if (j < w) before += P.wave[j];
         total += P.wave[j];
     }
-    __syncthreads();
     return before + x;
 }
 
-// Units of all batch rows, and of those before batch row `stop`.
-__device__ inline long long units_total(const AttnParams& A, Plan& P, int stop, long long& before) {
-    const int t = static_cast<int>(threadIdx.x);
-    long long all = 0, pre = 0;
-    for (int b = t; b < A.c.B; b += NTQ) {
-        const int u = seq_of(A, b).units;
-        all += u;
-        if (b < stop) pre += u;
+// The batch's units, cut into `ranges` contiguous ranges whose sizes differ by at most one.
+struct Ranges {
+    long long size, more;                                  // the first `more` ranges hold size + 1
+    int ranges;
+    __device__ long long start(int w) const { return size * w + (w < more ? w : more); }
+    __device__ int holding(long long u) const {
+        const long long c = more * (size + 1);
+        return static_cast<int>(u < c ? u / (size + 1) : more + (u - c) / size);
     }
-    long long total;
-    block_inclusive(P, pre, before);
-    block_inclusive(P, all, total);
-    return total;
-}
+};
 
-// The batch row that holds unit `target` (< the total) and the units before it.
-__device__ inline int units_find(const AttnParams& A, Plan& P, long long target, long long& pre) {
-    const int t = static_cast<int>(threadIdx.x);
-    long long run = 0;
-    for (int b0 = 0; b0 < A.c.B; b0 += NTQ) {
-        const int u = b0 + t < A.c.B ? seq_of(A, b0 + t).units : 0;
-        long long total;
-        const long long inc = run + block_inclusive(P, u, total);
+// What join_kernel needs of a batch row (of the row in which range w starts).
+struct RangeRec {
+    long long pre;             // units before it
+    int units, b;
+};
+constexpr size_t REC_AT = 64;  // bytes of the workspace before the records: a Ranges
+
+// Where range w starts: batch row, units before it. The same in every lane.
+__device__ inline Ranges locate(const AttnParams& A, Plan& P, int w, int& b, long long& pre) {
+    const int t = static_cast<int>(threadIdx.x), B = A.c.B;
+    int u = t < B ? seq_of(A, t).units : 0;
+    long long chunk, inc = block_inclusive(P, u, chunk), total = chunk;
+    if (B > NTQ) {
+        long long rest = 0, sum;
+        for (int j = t + NTQ; j < B; j += NTQ) rest += seq_of(A, j).units;
+        block_inclusive(P, rest, sum);
+        total += sum;
+    }
+    Ranges r;
+    r.ranges = total < A.W ? static_cast<int>(total) : A.W;
+    r.size = total / r.ranges;
+    r.more = total - r.size * r.ranges;
+    if (w >= r.ranges) return r;
+    const long long target = r.start(w);
+    if (target >= inc - u && target < inc) { P.b = t; P.pre = inc - u; }
+    long long run = chunk;
+    for (int b0 = NTQ; run <= target; b0 += NTQ) {
+        u = b0 + t < B ? seq_of(A, b0 + t).units : 0;
+        inc = run + block_inclusive(P, u, chunk);
         if (target >= inc - u && target < inc) { P.b = b0 + t; P.pre = inc - u; }
-        run += total;
-        if (target < run) break;
+        run += chunk;
     }
     __syncthreads();
+    b = P.b;
     pre = P.pre;
-    const int b = P.b;
-    __syncthreads();
-    return b;
+    return r;
 }
 
-__device__ inline long long range_start(const AttnParams& A, long long total, int w) { return total * w / A.W; }
+// Loads into LDS are waited for by hand (wait_loads): the compiler would have each LDS
+// read wait for every load in flight, since they go to one array. It does so unless it
+// cannot tell that a load's destination is that array.
+__device__ inline lds_ptr untraced(lds_ptr p) {
+    asm volatile("" : "+r"(p));
+    return p;
+}
 
 // s_waitcnt: at most `vm` loads in flight / no LDS read in flight; nothing moves across
 template <int VM>
@@ -330,6 +353,14 @@ __device__ inline void wait_lds() {
     __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+}
+
+// 2^(x - m) for x whose maximum m is (within 2^8 in weight): the difference of the rounded
+// scores. Fused with the multiplication that gave x it would hold x's rounding error,
+// which for scores beyond 2^30 is a power of two that overflows.
+__device__ inline float exp2_diff(float x, float m) {
+#pragma clang fp contract(off)
+    return __builtin_amdgcn_exp2f(x - m);
 }
 
 template <class T>
@@ -396,7 +427,7 @@ struct TileShape {
     static constexpr int RPI_SHIFT = RPI == 16 ? 4 : RPI == 8 ? 3 : RPI == 4 ? 2 : 1;
     static constexpr int NL = TT / RPI;                    // load instructions per tile
     static constexpr int KB = TT * RB;                     // bytes of a tile
-    static constexpr int LDS = NWQ * 2 * KB;
+    static constexpr int STAGE = NWQ * 2 * KB;             // keys and values of every wave's tile
     // Row r's chunk c sits at place c ^ swz(r), so that the 16 lanes that read one
     // chunk of 16 consecutive rows touch 16 different 16-byte columns of the banks.
     __device__ static inline int swz(int r) {
@@ -405,20 +436,27 @@ struct TileShape {
 };
 
 // Workgroups per CU (waves per SIMD): as many as LDS and the registers allow: the
-// accumulators, the queries, scores and weights, and about 70 for the rest.
+// accumulators, the queries, scores and weights, one tile's operands and about 70 more.
+constexpr int LDS_CU = 160 * 1024, LDS_MORE = 3 * 1024;    // per CU; a workgroup's beside the tiles
 template <int D, int MT, bool E4M3>
 constexpr int attn_occupancy() {
-    constexpr int lds = 160 * 1024 / (TileShape<D, E4M3>::LDS + 3 * 1024);
-    constexpr int regs = 512 / (D * MT / 4 + D * MT / 8 + 12 * MT + 70);
-    return lds < regs ? lds : regs < 4 ? regs : 4;
+    constexpr int lds = LDS_CU / (TileShape<D, E4M3>::STAGE + LDS_MORE);
+    constexpr int regs = 512 / (D * MT / 4 + D * MT / 8 + 12 * MT + D / (E4M3 ? 8 : 4) + 70);
+    return lds < regs ? lds : regs < 4 ? regs < 1 ? 1 : regs : 4;
+}
+// Tiles of a wave in LDS: the more loads in flight, the nearer to HBM's rate.
+template <int D, int MT, bool E4M3>
+constexpr int attn_stages() {
+    constexpr int n = (LDS_CU / attn_occupancy<D, MT, E4M3>() - LDS_MORE) / TileShape<D, E4M3>::STAGE;
+    return n < 2 ? 1 : 2;
 }
 
 template <class T, int D, int MT, bool E4M3>
 __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_kernel(AttnParams A) {
     using S = TileShape<D, E4M3>;
     constexpr int M16 = 16 * MT, ND = D / 16, NC = D / 32;
-    // two arrays, so that the compiler knows that a load into one does not write the other
-    __shared__ __attribute__((aligned(16))) unsigned char lds_k[NWQ * S::KB], lds_v[NWQ * S::KB];
+    constexpr int NS = attn_stages<D, MT, E4M3>();
+    __shared__ __attribute__((aligned(16))) unsigned char lds[NS * S::STAGE];
     __shared__ float st_m[NWQ][M16], st_l[NWQ][M16], fin[M16];
     __shared__ Plan plan;
     __shared__ int odd_any;                                // some edge value was not finite
@@ -430,21 +468,20 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
     const int x = static_cast<int>(blockIdx.x) / per * 8 + sub % 8, mb = sub / 8;
     if (x >= A.W * C.Hkv) return;
     const int h = x % C.Hkv, w = x / C.Hkv;
-    long long total, pre;
-    {
-        long long unused;
-        total = units_total(A, plan, 0, unused);
-    }
-    long long at = range_start(A, total, w);
-    const long long end = range_start(A, total, w + 1);
-    if (at >= end) return;
-    int b = units_find(A, plan, at, pre);
-
     if (t == 0) odd_any = 0;
-    __syncthreads();
+    int b = 0;
+    long long pre = 0;
+    const Ranges ranges = locate(A, plan, w, b, pre);
+    if (w >= ranges.ranges) return;
+    long long at = ranges.start(w);
+    const long long end = ranges.start(w + 1);
+    RangeRec* recs = reinterpret_cast<RangeRec*>(reinterpret_cast<char*>(A.ws) + REC_AT);
+    const bool scribe = A.W > 1 && h == 0 && mb == 0 && t == 0;
+    if (scribe && w == 0) *reinterpret_cast<Ranges*>(A.ws) = ranges;
+    bool first = true;
 
-    unsigned char* kt = lds_k + wv * S::KB;
-    unsigned char* vt = lds_v + wv * S::KB;
+
+    unsigned char* tiles_at = lds + wv * (NS * 2 * S::KB); // [stage][keys, values]
     const char* kbase = C.k + h * C.ks[1];
     const char* vbase = C.v + h * C.vs[1];
     const float ksc = E4M3 ? C.k_scale[h] : 1.0f, vsc = E4M3 ? C.v_scale[h] : 1.0f;
@@ -461,6 +498,8 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
         const int u0 = __builtin_amdgcn_readfirstlane(static_cast<int>(at - pre));
         const int u1 = __builtin_amdgcn_readfirstlane(static_cast<int>(end - pre < units ? end - pre : units));
         at += u1 - u0;
+        if (scribe && (A.direct ? u0 == 0 : first)) recs[A.direct ? b : w] = RangeRec{pre, units, b};
+        first = false;
         if (n_tok == 0) {                                  // bad lengths: one unit, NaN
             for (int i = t; i < M16 * D; i += NTQ) {
                 const int m = m0 + i / D;
@@ -499,7 +538,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                     const int slot = (beg + tile * TT + j * S::RPI) & slot_mask;
                     const char* src = cache + page * str[0] + slot * str[2];
                     const unsigned off = row_off + static_cast<unsigned>((lane % S::CPR) ^ S::swz(j * S::RPI + lrow)) * 16u;
-                    __builtin_amdgcn_global_load_lds((glb_ptr)(src + off), (lds_ptr)(dst + j * 1024), 16, 0, 0);
+                    __builtin_amdgcn_global_load_lds((glb_ptr)(src + off), untraced((lds_ptr)(dst + j * 1024)), 16, 0, 0);
                 }
             } else {
 #pragma unroll 1
@@ -509,17 +548,21 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                     const int slot = key_of(tile, row) & slot_mask;
                     const int chunk = (lane % S::CPR) ^ S::swz(row);
                     const char* src = cache + page * str[0] + slot * str[2] + chunk * 16;
-                    __builtin_amdgcn_global_load_lds((glb_ptr)src, (lds_ptr)(dst + j * 1024), 16, 0, 0);
+                    __builtin_amdgcn_global_load_lds((glb_ptr)src, untraced((lds_ptr)(dst + j * 1024)), 16, 0, 0);
                 }
             }
         };
-        int tile = wv;
-        int page1 = 0;
+        int tile = wv, stage = 0;
+        int pages = 0;                                     // of the next tile to load
         if (tile < tiles) {
-            const int page0 = page_of(tile);
-            page1 = page_of(tile + NWQ);
-            issue(kt, kbase, C.ks, tile, page0);
-            issue(vt, vbase, C.vs, tile, page0);
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                if (tile + j * NWQ >= tiles) break;
+                const int now = page_of(tile + j * NWQ);
+                issue(tiles_at + j * 2 * S::KB, kbase, C.ks, tile + j * NWQ, now);
+                issue(tiles_at + j * 2 * S::KB + S::KB, vbase, C.vs, tile + j * NWQ, now);
+            }
+            pages = page_of(tile + NS * NWQ);              // (past the last tile: the last key's)
         }
         // this lane's query rows: the MFMA's B operand, and where each one stands
         i32x4 qf[MT][NC];
@@ -549,43 +592,47 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
 #pragma unroll
             for (int d = 0; d < ND; ++d) acc[d][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        // one tile; MORE: the wave has another, whose loads are issued as places get free
-        auto step = [&](auto MORE) {
-            constexpr bool more = decltype(MORE)::value;
+        // One tile of which LEFT more are in LDS or on their way, NS if another is to be
+        // loaded behind them. Loads in flight are counted in their order: keys and values
+        // of a tile, then of the next. A place is refilled as soon as its operands are read.
+        auto step = [&](auto LEFT) {
+            constexpr int left = decltype(LEFT)::value;
+            constexpr bool more = left == NS;
+            unsigned char* kt = tiles_at + (NS > 1 ? stage : 0) * 2 * S::KB;
+            unsigned char* vt = kt + S::KB;
             const int tok = beg + tile * TT, ro = opaque(r16), go = opaque(g);
-            wait_loads<S::NL>();                           // the keys are in, the values may not be
+            wait_loads<(more ? 2 * NS - 1 : 2 * left + 1) * S::NL>();      // the keys are in
+            i32x4 kf[2][E4M3 ? NC / 2 : NC];
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const int row = 16 * a + ro;
+#pragma unroll
+                for (int c = 0; c < (E4M3 ? NC / 2 : NC); ++c)
+                    kf[a][c] = *reinterpret_cast<const i32x4*>(kt + row * S::RB + ((c * 4 + go) ^ S::swz(row)) * 16);
+            }
+            wait_lds();                                    // their place is free
+            const int pages_now = pages;
+            if constexpr (more) {
+                issue(kt, kbase, C.ks, tile + NS * NWQ, pages_now);
+                pages = page_of(tile + (NS + 1) * NWQ);
+            }
             f32x4 sc[2][MT];
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) sc[a][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                const int row = 16 * a + ro;
-                const unsigned char* kr = kt + row * S::RB;
-                if constexpr (E4M3) {
 #pragma unroll
-                    for (int c = 0; c < NC; c += 2) {
-                        const i32x4 k16 = *reinterpret_cast<const i32x4*>(kr + (((c / 2) * 4 + go) ^ S::swz(row)) * 16);
-                        const i32x4 k0 = widen8<T>(i32x2{k16.x, k16.y}), k1 = widen8<T>(i32x2{k16.z, k16.w});
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            sc[a][mt] = mfma<T>(k0, qf[mt][c], sc[a][mt]);
-                            sc[a][mt] = mfma<T>(k1, qf[mt][c + 1], sc[a][mt]);
-                        }
+                for (int c = 0; c < NC; ++c) {
+                    i32x4 k;
+                    if constexpr (E4M3) {
+                        const i32x4 k16 = kf[a][c / 2];
+                        k = widen8<T>(c & 1 ? i32x2{k16.z, k16.w} : i32x2{k16.x, k16.y});
+                    } else {
+                        k = kf[a][c];
                     }
-                } else {
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const i32x4 kf = *reinterpret_cast<const i32x4*>(kr + ((c * 4 + go) ^ S::swz(row)) * 16);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) sc[a][mt] = mfma<T>(kf, qf[mt][c], sc[a][mt]);
-                    }
+                    for (int mt = 0; mt < MT; ++mt) sc[a][mt] = mfma<T>(k, qf[mt][c], sc[a][mt]);
                 }
-            }
-            wait_lds();                                    // the keys' place is free
-            int page2 = 0;
-            if constexpr (more) {
-                page2 = page_of(tile + 2 * NWQ);           // (past the last tile: the last key's)
-                issue(kt, kbase, C.ks, tile + NWQ, page1);
             }
             // scores in units of log2, masked
             const bool edge = tok + TT - 1 > kv || (A.window > 0 && tok <= hi - 1 - A.window);
@@ -599,10 +646,11 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                         sc[j / 4][mt][j % 4] = c - 2.0f * c * __builtin_amdgcn_rcpf(1.0f + e);
                     }
             } else {
+                const float factor = scale * LOG2E;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sc[j / 4][mt][j % 4] *= scale * LOG2E;
+                    for (int j = 0; j < 8; ++j) sc[j / 4][mt][j % 4] *= factor;
             }
             if (A.slopes) {
 #pragma unroll
@@ -655,7 +703,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                     float p[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        p[r] = __builtin_amdgcn_exp2f(sc[a][mt][r] - mx[mt]);
+                        p[r] = exp2_diff(sc[a][mt][r], mx[mt]);
                         sum[mt] += p[r];
                     }
                     // rounded once to the operand type of the matrix cores
@@ -663,26 +711,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                     pf[mt][2 * a + 1] = static_cast<int>(pack2<T>(p[2], p[3]));
                 }
             }
-            wait_loads<more ? S::NL : 0>();                // the values are in
-            // columns 16 d .. 16 d + 15 of the values as the MFMA's A operand
-            auto value = [&](int d) {
-                i32x4 vf;
-                if constexpr (E4M3) {
-                    const int rr = ro >> 1, row = rr < 4 ? 4 * go + rr : 12 + 4 * go + rr;
-                    vf = widen8<T>(__builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                        (lds_i32x2)(vt + row * S::RB + (d ^ S::swz(row)) * 16 + (ro & 1) * 8)));
-                } else {
-#pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        const int row = 16 * a + 4 * go + (ro >> 2), c = 2 * d + ((ro >> 1) & 1);
-                        const i32x2 v = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (lds_i16x4)(vt + row * S::RB + (c ^ S::swz(row)) * 16 + (ro & 1) * 8)));
-                        vf[2 * a] = v.x;
-                        vf[2 * a + 1] = v.y;
-                    }
-                }
-                return vf;
-            };
+            wait_loads<(more ? 2 * NS - 1 : 2 * left) * S::NL>();          // the values are in
             if (edge) {
                 // A weight of zero does not cancel a value that is not finite. Values that
                 // nobody sees become zeros; of those that only some rows see what is not
@@ -699,22 +728,42 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                 }
                 wait_lds();
             }
+            // columns 16 d .. 16 d + 15 of the values as the MFMA's A operand
+            i32x2 vf[ND][E4M3 ? 1 : 2];
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                const i32x4 vf = value(d);
+                if constexpr (E4M3) {
+                    const int rr = ro >> 1, row = rr < 4 ? 4 * go + rr : 12 + 4 * go + rr;
+                    vf[d][0] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                        (lds_i32x2)(vt + row * S::RB + (d ^ S::swz(row)) * 16 + (ro & 1) * 8));
+                } else {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) acc[d][mt] = mfma<T>(vf, pf[mt], acc[d][mt]);
+                    for (int a = 0; a < 2; ++a) {
+                        const int row = 16 * a + 4 * go + (ro >> 2), c = 2 * d + ((ro >> 1) & 1);
+                        vf[d][a] = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (lds_i16x4)(vt + row * S::RB + (c ^ S::swz(row)) * 16 + (ro & 1) * 8)));
+                    }
+                }
             }
-            wait_lds();                                    // the values' place is free
-            if constexpr (more) {
-                issue(vt, vbase, C.vs, tile + NWQ, page1);
-                page1 = page2;
-                tile += NWQ;
+            wait_lds();                                    // their place is free
+            if constexpr (more) issue(vt, vbase, C.vs, tile + NS * NWQ, pages_now);
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                i32x4 v;
+                if constexpr (E4M3) v = widen8<T>(vf[d][0]);
+                else v = i32x4{vf[d][0].x, vf[d][0].y, vf[d][1].x, vf[d][1].y};
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) acc[d][mt] = mfma<T>(v, pf[mt], acc[d][mt]);
             }
+            tile += NWQ;
+            if (NS > 1) stage = stage + 1 < NS ? stage + 1 : 0;
         };
         if (tile < tiles) {
-            while (tile + NWQ < tiles) step(Bool<true>());
-            step(Bool<false>());
+            while (tile + NS * NWQ < tiles) step(Int<NS>());
+            if constexpr (NS > 1) {
+                if (tile + NWQ < tiles) step(Int<1>());
+            }
+            step(Int<0>());
         }
         // ---- join the four waves
         const bool nan = __any(bad);
@@ -731,7 +780,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
         }
         __syncthreads();                                   // the statistics are in, the tiles are free
         const bool odd = odd_any != 0;
-        float* slot = A.ws + (static_cast<long long>(w * C.Hkv + h) * A.MB + mb) * (2ll * M16 * (D + 2)) +
+        float* slot = A.ws + A.slots_at + (static_cast<long long>(w * C.Hkv + h) * A.MB + mb) * (2ll * M16 * (D + 2)) +
                       (u0 == 0 ? M16 * (D + 2) : 0);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -753,32 +802,25 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                 }
             }
         }
-        // waves 0 and 1 exchange in the keys' array, 2 and 3 in the values': [2][M16][16 DC] each
-        constexpr int FIT = S::KB * NWQ / (2 * M16 * 64);  // 16-element column blocks that fit
+        constexpr int FIT = NS * S::STAGE / (NWQ * M16 * 64);      // 16-element column blocks that fit
         constexpr int DC = FIT >= ND ? ND : FIT >= 8 ? 8 : FIT >= 4 ? 4 : FIT >= 2 ? 2 : 1;
-        static_assert(FIT >= 1 && NWQ == 4, "exchange");
-        float* ex0 = reinterpret_cast<float*>(lds_k);
-        float* ex1 = reinterpret_cast<float*>(lds_v);
+        static_assert(FIT >= 1, "exchange");
+        float* ex = reinterpret_cast<float*>(lds);         // [wave][M16][16 DC]
 #pragma unroll
         for (int d0 = 0; d0 < ND; d0 += DC) {
 #pragma unroll
             for (int d = 0; d < DC; ++d)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float* ex = wv < 2 ? ex0 : ex1;
-                    *reinterpret_cast<f32x4*>(ex + (((wv & 1) * M16 + mt * 16 + r16) * DC + d) * 16 + 4 * g) =
-                        acc[d0 + d][mt];
-                }
+                for (int mt = 0; mt < MT; ++mt)
+                    *reinterpret_cast<f32x4*>(ex + ((wv * M16 + mt * 16 + r16) * DC + d) * 16 + 4 * g) = acc[d0 + d][mt];
             __syncthreads();
             if (t == 0) odd_any = 0;                       // (everyone has read it)
             for (int i = t; i < M16 * DC * 4; i += NTQ) {
                 const int m = i / (DC * 4), d = d0 * 16 + i % (DC * 4) * 4;
                 if (m0 + m >= A.M) continue;
-                const int half = M16 * DC * 16;
-                f32x4 o = (*reinterpret_cast<const f32x4*>(ex0 + 4 * i) +
-                           *reinterpret_cast<const f32x4*>(ex0 + half + 4 * i)) +
-                          (*reinterpret_cast<const f32x4*>(ex1 + 4 * i) +
-                           *reinterpret_cast<const f32x4*>(ex1 + half + 4 * i));
+                f32x4 o = *reinterpret_cast<const f32x4*>(ex + 4 * i);
+#pragma unroll
+                for (int j = 1; j < NWQ; ++j) o += *reinterpret_cast<const f32x4*>(ex + j * M16 * DC * 16 + 4 * i);
                 if (odd) {
                     const int at_pos = kv + min((m0 + m) / A.G, n_tok - 1);
                     const int from = max(beg, lo), past = min(stop, hi), seen_by_all = hi - A.window;
@@ -818,59 +860,91 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
     }
 }
 
-// Merges the pieces of a sequence that crosses ranges: one workgroup per cache head,
-// row block, group of query rows and batch row (or, with more batch rows than
-// ranges, border between ranges: the first border inside a sequence stands for it).
+// Merges the pieces of every sequence that crosses ranges. A workgroup takes some rows of
+// one sequence: those of a batch row or, when there are at least as many batch rows as
+// ranges, of the sequence that the border before range w cuts (the first border inside
+// a sequence stands for it). D / 4 threads hold a row; `slices` of such groups share its
+// pieces, four loads of each in flight, and meet in LDS.
 template <class T>
 __global__ __launch_bounds__(NTQ) void join_kernel(AttnParams A) {
-    __shared__ Plan plan;
+    __shared__ float st[NTQ][2];
+    __shared__ f32x4 so[NTQ];
     const Cache& C = A.c;
-    const int t = static_cast<int>(threadIdx.x), cols = A.D / 4, rows = NTQ / cols;
+    const int t = static_cast<int>(threadIdx.x), cols = A.D / 4, rows = NTQ / cols / A.slices;
     const int groups = (A.M16 + rows - 1) / rows;
     int x = static_cast<int>(blockIdx.x);
     const int gr = x % groups; x /= groups;
     const int mb = x % A.MB; x /= A.MB;
     const int h = x % C.Hkv; x /= C.Hkv;
-    int b = x;
-    long long pre;
-    const long long total = units_total(A, plan, b, pre);
-    if (!A.direct) {
-        const long long border = range_start(A, total, x + 1);
-        if (border >= total) return;
-        b = units_find(A, plan, border, pre);
-        if (border == pre || range_start(A, total, x) > pre) return;
-    }
-    const Seq s = seq_of(A, b);
-    const long long fin = pre + s.units;
-    // the first and the last range that hold units of the sequence
-    const int wa = static_cast<int>(((pre + 1) * A.W + total - 1) / total) - 1;
-    const int wb = static_cast<int>((fin * A.W + total - 1) / total) - 1;
+    const Ranges r = *reinterpret_cast<const Ranges*>(A.ws);
+    if (!A.direct && x + 1 >= r.ranges) return;
+    const RangeRec rec = reinterpret_cast<const RangeRec*>(reinterpret_cast<const char*>(A.ws) + REC_AT)[A.direct ? x : x + 1];
+    if (!A.direct && (r.start(x + 1) == rec.pre || r.start(x) > rec.pre)) return;
+    const int wa = r.holding(rec.pre), wb = r.holding(rec.pre + rec.units - 1);
     if (wa >= wb) return;
-    const int m = gr * rows + t / cols, d = t % cols * 4, tk = (mb * A.M16 + m) / A.G;
-    if (m >= A.M16 || mb * A.M16 + m >= A.M) return;
+    const int col = t % cols, row = t / cols % rows, sl = t / cols / rows;
+    const int m = gr * rows + row, q = mb * A.M16 + m;
+    const bool live = m < A.M16 && q < A.M;
     const long long size = static_cast<long long>(A.M16) * (A.D + 2);
     float n = -F32_MAX, l = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int w = wa; w <= wb; ++w) {
-        const long long from = range_start(A, total, w);
-        if (from >= range_start(A, total, w + 1)) continue;
-        const float* slot = A.ws + ((static_cast<long long>(w) * C.Hkv + h) * A.MB + mb) * 2 * size +
-                            (from <= pre ? size : 0);
-        const float pm = slot[A.M16 * A.D + 2 * m], pl = slot[A.M16 * A.D + 2 * m + 1];
-        const f32x4 po = *reinterpret_cast<const f32x4*>(slot + m * A.D + d);
-        const float nn = fmaxf(n, pm), f = __builtin_amdgcn_exp2f(n - nn), pf = __builtin_amdgcn_exp2f(pm - nn);
+    for (int w0 = wa + sl; live && w0 <= wb; w0 += 4 * A.slices) {
+        float pm[4], pl[4];
+        f32x4 po[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int w = w0 + j * A.slices;
+            pm[j] = -F32_MAX;
+            pl[j] = 0.0f;
+            po[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (w <= wb) {
+                const float* slot = A.ws + A.slots_at + ((static_cast<long long>(w) * C.Hkv + h) * A.MB + mb) * 2 * size +
+                                    (r.start(w) <= rec.pre ? size : 0);
+                pm[j] = slot[A.M16 * A.D + 2 * m];
+                pl[j] = slot[A.M16 * A.D + 2 * m + 1];
+                po[j] = *reinterpret_cast<const f32x4*>(slot + m * A.D + col * 4);
+            }
+        }
+        float nn = n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) nn = fmaxf(nn, pm[j]);
+        const float f = __builtin_amdgcn_exp2f(n - nn);
+        l *= f;
+        o *= f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float e = __builtin_amdgcn_exp2f(pm[j] - nn);
+            l += pl[j] * e;
+            o += po[j] * e;
+        }
         n = nn;
-        l = l * f + pl * pf;
-        o = o * f + po * pf;
     }
+    if (A.slices > 1) {
+        st[t][0] = n;
+        st[t][1] = l;
+        so[t] = o;
+        __syncthreads();
+        if (sl > 0) return;
+        for (int j = 1; j < A.slices; ++j) {
+            const int u = t + j * cols * rows;
+            const float nn = fmaxf(n, st[u][0]);
+            const float f = __builtin_amdgcn_exp2f(n - nn), e = __builtin_amdgcn_exp2f(st[u][0] - nn);
+            n = nn;
+            l = l * f + st[u][1] * e;
+            o = o * f + so[u] * e;
+        }
+    }
+    if (!live) return;
+    int kv;
     u32x2 y = {0, 0};
-    if (tk < s.n) {
+    const int tk = q / A.G, n_tok = seq_rows(C, rec.b, kv);
+    if (tk < n_tok) {
         const float inv = (C.v_scale ? C.v_scale[h] : 1.0f) / l;
         y.x = pack2<T>(o.x * inv, o.y * inv);
         y.y = pack2<T>(o.z * inv, o.w * inv);
     }
-    const long long row = (static_cast<long long>(b) * C.R + tk) * A.Hq + h * A.G + (mb * A.M16 + m) % A.G;
-    *reinterpret_cast<u32x2*>(A.out + (row * A.D + d) * 2) = y;
+    const long long at = (static_cast<long long>(rec.b) * C.R + tk) * A.Hq + h * A.G + q % A.G;
+    *reinterpret_cast<u32x2*>(A.out + (at * A.D + col * 4) * 2) = y;
 }
 
 // ------------------------------------------------------------------ logit adjustment
@@ -1151,7 +1225,7 @@ int check_cache(int dtype, int32_t B, int32_t R, int32_t max_R, int32_t Hkv, int
 // Row blocks, ranges and workspace of an attention call.
 struct AttnPlan {
     int M, MB, MT, W;
-    size_t bytes;
+    size_t slots_at, bytes;
 };
 
 int attn_occupancy_of(int D, int MT, bool e4m3) {
@@ -1175,7 +1249,8 @@ AttnPlan attn_plan(int B, int R, int Hq, int Hkv, int D, bool e4m3, int page_siz
     const long long units = B * ((static_cast<long long>(max_pages) * page_size + TT + TU - 1) / TU);
     if (w > units) w = units;
     p.W = w < 1 ? 1 : static_cast<int>(w);
-    p.bytes = static_cast<size_t>(lanes) * p.W * 2 * 16 * p.MT * (D + 2) * sizeof(float);
+    p.slots_at = (REC_AT + p.W * sizeof(RangeRec) + 255) & ~static_cast<size_t>(255);
+    p.bytes = p.slots_at + static_cast<size_t>(lanes) * p.W * 2 * 16 * p.MT * (D + 2) * sizeof(float);
     p.bytes = p.W == 1 ? 256 : (p.bytes + 255) & ~static_cast<size_t>(255);
     return p;
 }
@@ -1206,8 +1281,7 @@ int launch_attn(AttnParams& A, int MT, bool e4m3, hipStream_t s) {
     else launch_attn_d<T, 256>(A, MT, e4m3, static_cast<unsigned>(grid), s);
     const int rc = launched();
     if (rc != SPEC_OK || A.W == 1) return rc;              // one range: nothing crosses
-    A.direct = A.c.B < A.W;
-    const int rows = NTQ / (A.D / 4), groups = (A.M16 + rows - 1) / rows;
+    const int rows = NTQ / (A.D / 4) / A.slices, groups = (A.M16 + rows - 1) / rows;
     const long long join = static_cast<long long>(A.direct ? A.c.B : A.W - 1) * A.c.Hkv * A.MB * groups;
     hipLaunchKernelGGL((join_kernel<T>), dim3(static_cast<unsigned>(join)), dim3(NTQ), 0, s, A);
     return launched();
@@ -1293,6 +1367,11 @@ int spec_attention(const void* q, const int64_t* q_stride, int dtype, int32_t B,
     A.scale = scale; A.softcap = softcap; A.window = window;
     A.Hq = Hq; A.G = Hq / Hkv; A.D = D;
     A.M = plan.M; A.MB = plan.MB; A.M16 = 16 * plan.MT; A.W = plan.W;
+    A.slots_at = static_cast<long long>(plan.slots_at / sizeof(float));
+    A.direct = B < plan.W;
+    // a sequence has about W / B pieces
+    A.slices = 1;
+    while (A.slices < NTQ / (D / 4) && A.slices * B < plan.W) A.slices *= 2;
     hipStream_t s = static_cast<hipStream_t>(stream);
     return dtype == SPEC_DTYPE_BF16 ? launch_attn<Bf16>(A, plan.MT, e4m3, s) : launch_attn<F16>(A, plan.MT, e4m3, s);
 }
