@@ -193,6 +193,7 @@ constexpr int NWQ = NTQ / 64;
 constexpr int TT = 32;                                     // keys of a wave's tile
 constexpr int TU = TT * NWQ;                               // keys of a unit
 constexpr int CUS = 256;
+constexpr int NT_LOAD = 2;                                 // cache policy: non-temporal (read once)
 constexpr float LAZY = 8.0f;                               // log2 of the largest weight
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -209,7 +210,7 @@ struct AttnParams {
     long long qs[3];           // bytes between batch rows, tokens, heads
     const float* slopes;       // [Hq] or null
     char* out;                 // [B, R, Hq, D]
-    float* ws;                 // a Ranges, W RangeRec, then per (w, head, block): two slots of M16 * (D + 2) floats
+    float* ws;                 // W RangeRec, then per (w, head, block): two slots of M16 * (D + 2) floats
     long long slots_at;        // floats before the slots
     float scale, softcap;
     int window, Hq, G, D;
@@ -288,6 +289,7 @@ __device__ inline long long block_inclusive(Plan& P, long long v, long long& tot
 struct Ranges {
     long long size, more;                                  // the first `more` ranges hold size + 1
     int ranges;
+
     __device__ long long start(int w) const { return size * w + (w < more ? w : more); }
     __device__ int holding(long long u) const {
         const long long c = more * (size + 1);
@@ -295,12 +297,12 @@ struct Ranges {
     }
 };
 
-// What join_kernel needs of a batch row (of the row in which range w starts).
+// What join_kernel needs of a batch row (of the row in which range w starts): the first and
+// last range that hold units of it. Each of them has a piece of it in its slot 0, the
+// first range, where the row begins, in its slot 1.
 struct RangeRec {
-    long long pre;             // units before it
-    int units, b;
+    int b, n_tok, wa, wb;
 };
-constexpr size_t REC_AT = 64;  // bytes of the workspace before the records: a Ranges
 
 // Where range w starts: batch row, units before it. The same in every lane.
 __device__ inline Ranges locate(const AttnParams& A, Plan& P, int w, int& b, long long& pre) {
@@ -448,7 +450,7 @@ constexpr int attn_occupancy() {
 template <int D, int MT, bool E4M3>
 constexpr int attn_stages() {
     constexpr int n = (LDS_CU / attn_occupancy<D, MT, E4M3>() - LDS_MORE) / TileShape<D, E4M3>::STAGE;
-    return n < 2 ? 1 : 2;
+    return n < 1 ? 1 : n > 4 ? 4 : n;
 }
 
 template <class T, int D, int MT, bool E4M3>
@@ -472,12 +474,14 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
     int b = 0;
     long long pre = 0;
     const Ranges ranges = locate(A, plan, w, b, pre);
-    if (w >= ranges.ranges) return;
+    RangeRec* recs = reinterpret_cast<RangeRec*>(A.ws);
+    const bool scribe = A.W > 1 && h == 0 && mb == 0 && t == 0;
+    if (w >= ranges.ranges) {
+        if (scribe && !A.direct) recs[w] = RangeRec{0, 0, -1, -1};
+        return;
+    }
     long long at = ranges.start(w);
     const long long end = ranges.start(w + 1);
-    RangeRec* recs = reinterpret_cast<RangeRec*>(reinterpret_cast<char*>(A.ws) + REC_AT);
-    const bool scribe = A.W > 1 && h == 0 && mb == 0 && t == 0;
-    if (scribe && w == 0) *reinterpret_cast<Ranges*>(A.ws) = ranges;
     bool first = true;
 
 
@@ -498,7 +502,8 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
         const int u0 = __builtin_amdgcn_readfirstlane(static_cast<int>(at - pre));
         const int u1 = __builtin_amdgcn_readfirstlane(static_cast<int>(end - pre < units ? end - pre : units));
         at += u1 - u0;
-        if (scribe && (A.direct ? u0 == 0 : first)) recs[A.direct ? b : w] = RangeRec{pre, units, b};
+        if (scribe && (A.direct ? u0 == 0 : first))
+            recs[A.direct ? b : w] = RangeRec{b, n_tok, ranges.holding(pre), ranges.holding(pre + units - 1)};
         first = false;
         if (n_tok == 0) {                                  // bad lengths: one unit, NaN
             for (int i = t; i < M16 * D; i += NTQ) {
@@ -538,7 +543,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                     const int slot = (beg + tile * TT + j * S::RPI) & slot_mask;
                     const char* src = cache + page * str[0] + slot * str[2];
                     const unsigned off = row_off + static_cast<unsigned>((lane % S::CPR) ^ S::swz(j * S::RPI + lrow)) * 16u;
-                    __builtin_amdgcn_global_load_lds((glb_ptr)(src + off), untraced((lds_ptr)(dst + j * 1024)), 16, 0, 0);
+                    __builtin_amdgcn_global_load_lds((glb_ptr)(src + off), untraced((lds_ptr)(dst + j * 1024)), 16, 0, NT_LOAD);
                 }
             } else {
 #pragma unroll 1
@@ -548,7 +553,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                     const int slot = key_of(tile, row) & slot_mask;
                     const int chunk = (lane % S::CPR) ^ S::swz(row);
                     const char* src = cache + page * str[0] + slot * str[2] + chunk * 16;
-                    __builtin_amdgcn_global_load_lds((glb_ptr)src, untraced((lds_ptr)(dst + j * 1024)), 16, 0, 0);
+                    __builtin_amdgcn_global_load_lds((glb_ptr)src, untraced((lds_ptr)(dst + j * 1024)), 16, 0, NT_LOAD);
                 }
             }
         };
@@ -592,16 +597,15 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
 #pragma unroll
             for (int d = 0; d < ND; ++d) acc[d][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        // One tile of which LEFT more are in LDS or on their way, NS if another is to be
-        // loaded behind them. Loads in flight are counted in their order: keys and values
-        // of a tile, then of the next. A place is refilled as soon as its operands are read.
-        auto step = [&](auto LEFT) {
-            constexpr int left = decltype(LEFT)::value;
-            constexpr bool more = left == NS;
+        // One tile; MORE: NS tiles on the wave has another, loaded into this one's place as
+        // soon as its operands are read. Loads in flight are counted in their order: keys
+        // and values of a tile, then of the next.
+        auto step = [&](auto MORE) {
+            constexpr bool more = decltype(MORE)::value != 0;
             unsigned char* kt = tiles_at + (NS > 1 ? stage : 0) * 2 * S::KB;
             unsigned char* vt = kt + S::KB;
             const int tok = beg + tile * TT, ro = opaque(r16), go = opaque(g);
-            wait_loads<(more ? 2 * NS - 1 : 2 * left + 1) * S::NL>();      // the keys are in
+            wait_loads<(more ? (2 * NS - 1) * S::NL : NS > 1 ? 0 : S::NL)>();      // the keys are in
             i32x4 kf[2][E4M3 ? NC / 2 : NC];
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
@@ -711,7 +715,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                     pf[mt][2 * a + 1] = static_cast<int>(pack2<T>(p[2], p[3]));
                 }
             }
-            wait_loads<(more ? 2 * NS - 1 : 2 * left) * S::NL>();          // the values are in
+            wait_loads<(more ? (2 * NS - 1) * S::NL : 0)>();               // the values are in
             if (edge) {
                 // A weight of zero does not cancel a value that is not finite. Values that
                 // nobody sees become zeros; of those that only some rows see what is not
@@ -759,11 +763,8 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
             if (NS > 1) stage = stage + 1 < NS ? stage + 1 : 0;
         };
         if (tile < tiles) {
-            while (tile + NS * NWQ < tiles) step(Int<NS>());
-            if constexpr (NS > 1) {
-                if (tile + NWQ < tiles) step(Int<1>());
-            }
-            step(Int<0>());
+            while (tile + NS * NWQ < tiles) step(Int<1>());
+            do step(Int<0>()); while (tile < tiles);
         }
         // ---- join the four waves
         const bool nan = __any(bad);
@@ -876,12 +877,9 @@ __global__ __launch_bounds__(NTQ) void join_kernel(AttnParams A) {
     const int gr = x % groups; x /= groups;
     const int mb = x % A.MB; x /= A.MB;
     const int h = x % C.Hkv; x /= C.Hkv;
-    const Ranges r = *reinterpret_cast<const Ranges*>(A.ws);
-    if (!A.direct && x + 1 >= r.ranges) return;
-    const RangeRec rec = reinterpret_cast<const RangeRec*>(reinterpret_cast<const char*>(A.ws) + REC_AT)[A.direct ? x : x + 1];
-    if (!A.direct && (r.start(x + 1) == rec.pre || r.start(x) > rec.pre)) return;
-    const int wa = r.holding(rec.pre), wb = r.holding(rec.pre + rec.units - 1);
-    if (wa >= wb) return;
+    const RangeRec rec = reinterpret_cast<const RangeRec*>(A.ws)[A.direct ? x : x + 1];
+    const int wa = rec.wa, wb = rec.wb;
+    if (wa >= wb || (!A.direct && wa != x)) return;
     const int col = t % cols, row = t / cols % rows, sl = t / cols / rows;
     const int m = gr * rows + row, q = mb * A.M16 + m;
     const bool live = m < A.M16 && q < A.M;
@@ -899,7 +897,7 @@ __global__ __launch_bounds__(NTQ) void join_kernel(AttnParams A) {
             po[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             if (w <= wb) {
                 const float* slot = A.ws + A.slots_at + ((static_cast<long long>(w) * C.Hkv + h) * A.MB + mb) * 2 * size +
-                                    (r.start(w) <= rec.pre ? size : 0);
+                                    (w == wa ? size : 0);
                 pm[j] = slot[A.M16 * A.D + 2 * m];
                 pl[j] = slot[A.M16 * A.D + 2 * m + 1];
                 po[j] = *reinterpret_cast<const f32x4*>(slot + m * A.D + col * 4);
@@ -935,10 +933,9 @@ __global__ __launch_bounds__(NTQ) void join_kernel(AttnParams A) {
         }
     }
     if (!live) return;
-    int kv;
     u32x2 y = {0, 0};
-    const int tk = q / A.G, n_tok = seq_rows(C, rec.b, kv);
-    if (tk < n_tok) {
+    const int tk = q / A.G;
+    if (tk < rec.n_tok) {
         const float inv = (C.v_scale ? C.v_scale[h] : 1.0f) / l;
         y.x = pack2<T>(o.x * inv, o.y * inv);
         y.y = pack2<T>(o.z * inv, o.w * inv);
@@ -1249,7 +1246,7 @@ AttnPlan attn_plan(int B, int R, int Hq, int Hkv, int D, bool e4m3, int page_siz
     const long long units = B * ((static_cast<long long>(max_pages) * page_size + TT + TU - 1) / TU);
     if (w > units) w = units;
     p.W = w < 1 ? 1 : static_cast<int>(w);
-    p.slots_at = (REC_AT + p.W * sizeof(RangeRec) + 255) & ~static_cast<size_t>(255);
+    p.slots_at = (p.W * sizeof(RangeRec) + 255) & ~static_cast<size_t>(255);
     p.bytes = p.slots_at + static_cast<size_t>(lanes) * p.W * 2 * 16 * p.MT * (D + 2) * sizeof(float);
     p.bytes = p.W == 1 ? 256 : (p.bytes + 255) & ~static_cast<size_t>(255);
     return p;
