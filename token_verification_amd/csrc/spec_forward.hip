@@ -215,8 +215,8 @@ struct AttnParams {
     float scale, softcap;
     int window, Hq, G, D;
     int M;                     // R * G query rows per cache head
-    int MB;                    // row blocks of M16 = 16 * MT rows
-    int M16;
+    int MB;                    // row blocks of M16 rows
+    int M16;                   // query rows of a workgroup
     int W;                     // workgroups per cache head and row block
     int direct;                // join_kernel goes by batch row (else by border between ranges)
     int slices;                // join_kernel: threads that share a sequence's pieces
@@ -225,19 +225,26 @@ struct AttnParams {
 // a batch row's keys: positions [lo, hi) are seen by some token in use
 struct Seq {
     int kv, n;                 // first new position, tokens in use (0: bad lengths)
-    int lo, hi, base;          // base: lo rounded down to a tile
+    int lo, hi, base;          // base: lo rounded down to a tile of any shape
     int units;
 };
 
-__device__ inline Seq seq_of(const AttnParams& A, int b) {
+__device__ inline Seq seq_from(const AttnParams& A, int kv, int n) {
     Seq s;
-    s.n = seq_rows(A.c, b, s.kv);
-    if (s.n == 0) { s.lo = s.hi = s.base = 0; s.units = 1; return s; }
-    s.lo = A.window > 0 ? max(0, s.kv + 1 - A.window) : 0;
-    s.hi = s.kv + s.n;
-    s.base = s.lo & ~(TT - 1);
+    s.kv = kv;
+    s.n = n;
+    if (n == 0) { s.lo = s.hi = s.base = 0; s.units = 1; return s; }
+    s.lo = A.window > 0 ? max(0, kv + 1 - A.window) : 0;
+    s.hi = kv + n;
+    s.base = s.lo & ~(2 * TT - 1);                         // (the larger tile)
     s.units = (s.hi - s.base + TU - 1) / TU;
     return s;
+}
+
+__device__ inline Seq seq_of(const AttnParams& A, int b) {
+    int kv;
+    const int n = seq_rows(A.c, b, kv);
+    return seq_from(A, kv, n);
 }
 
 template <int N>
@@ -245,37 +252,31 @@ struct Int {
     static constexpr int value = N;
 };
 
-// x, which the compiler must not know: keeps the addresses that derive from it from being
-// computed before a loop and held in registers (dozens of them) throughout
-__device__ inline int opaque(int x) {
-    asm volatile("" : "+v"(x));
-    return x;
-}
-
 struct Plan {
-    long long wave[NWQ];
+    unsigned wave[NWQ];
     long long pre;
-    int b;
+    int b, kv, n;
 };
 
-__device__ inline long long wave_inclusive(long long v) {
+__device__ inline unsigned wave_inclusive(unsigned v) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const long long u = __shfl_up(v, d, 64);
+        const unsigned u = __shfl_up(v, d, 64);
         if (lane >= d) v += u;
     }
     return v;
 }
 
-// Inclusive scan over the workgroup of v; total is its sum.
-__device__ inline long long block_inclusive(Plan& P, long long v, long long& total) {
+// Inclusive scan over the workgroup of v; total is its sum (256 rows of at most 2^23 units
+// stay below 2^32).
+__device__ inline unsigned block_inclusive(Plan& P, unsigned v, unsigned& total) {
     const int w = threadIdx.x >> 6;
-    const long long x = wave_inclusive(v);
+    const unsigned x = wave_inclusive(v);
     __syncthreads();                                       // the last scan's sums have been read
     if ((threadIdx.x & 63) == 63) P.wave[w] = x;
     __syncthreads();
-    long long before = 0;
+    unsigned before = 0;
     total = 0;
 #pragma unroll
     for (int j = 0; j < NWQ; ++j) {
@@ -304,34 +305,77 @@ struct RangeRec {
     int b, n_tok, wa, wb;
 };
 
-// Where range w starts: batch row, units before it. The same in every lane.
-__device__ inline Ranges locate(const AttnParams& A, Plan& P, int w, int& b, long long& pre) {
+// x, the same in every lane, as a scalar
+__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ inline long long uniform(long long x) {
+    const unsigned lo = static_cast<unsigned>(uniform(static_cast<int>(x)));
+    const int hi = uniform(static_cast<int>(x >> 32));
+    return static_cast<long long>(static_cast<unsigned long long>(static_cast<unsigned>(hi)) << 32 | lo);
+}
+
+__device__ inline Ranges cut(long long total, int most) {
+    Ranges r;
+    r.ranges = total < most ? static_cast<int>(total) : most;
+    if (total <= 0x7fffffff) {
+        r.size = static_cast<int>(total) / r.ranges;
+    } else {
+        r.size = total / r.ranges;
+    }
+    r.more = total - r.size * r.ranges;
+    return r;
+}
+
+// Where range w starts: batch row (with its first new position and its tokens in use) and
+// the units before it. The same in every lane. Up to 64 batch rows each wave finds it by
+// itself; more are scanned by the workgroup, 256 at a time.
+__device__ inline Ranges locate(const AttnParams& A, Plan& P, int w, int& b, int& kv, int& n, long long& pre) {
     const int t = static_cast<int>(threadIdx.x), B = A.c.B;
-    int u = t < B ? seq_of(A, t).units : 0;
-    long long chunk, inc = block_inclusive(P, u, chunk), total = chunk;
-    if (B > NTQ) {
-        long long rest = 0, sum;
-        for (int j = t + NTQ; j < B; j += NTQ) rest += seq_of(A, j).units;
-        block_inclusive(P, rest, sum);
+    if (B <= 64) {
+        const int lane = t & 63;
+        int lkv = 0, ln = 0;
+        unsigned u = 0;
+        if (lane < B) {
+            ln = seq_rows(A.c, lane, lkv);
+            u = static_cast<unsigned>(seq_from(A, lkv, ln).units);
+        }
+        const unsigned inc = wave_inclusive(u);
+        const Ranges r = cut(uniform(static_cast<int>(__shfl(inc, 63, 64))), A.W);
+        const unsigned target = static_cast<unsigned>(r.start(w));
+        b = w < r.ranges ? uniform(__ffsll(__ballot(inc > target)) - 1) : 0;
+        kv = uniform(__shfl(lkv, b, 64));
+        n = uniform(__shfl(ln, b, 64));
+        pre = uniform(static_cast<int>(__shfl(inc - u, b, 64)));
+        return r;
+    }
+    Seq s;
+    s.kv = s.n = s.units = 0;
+    if (t < B) s = seq_of(A, t);
+    unsigned chunk, u = static_cast<unsigned>(s.units);
+    long long inc = block_inclusive(P, u, chunk), total = chunk;
+    for (int b0 = NTQ; b0 < B; b0 += NTQ) {
+        unsigned sum;
+        block_inclusive(P, b0 + t < B ? static_cast<unsigned>(seq_of(A, b0 + t).units) : 0u, sum);
         total += sum;
     }
-    Ranges r;
-    r.ranges = total < A.W ? static_cast<int>(total) : A.W;
-    r.size = total / r.ranges;
-    r.more = total - r.size * r.ranges;
+    const Ranges r = cut(uniform(total), A.W);
     if (w >= r.ranges) return r;
     const long long target = r.start(w);
-    if (target >= inc - u && target < inc) { P.b = t; P.pre = inc - u; }
-    long long run = chunk;
-    for (int b0 = NTQ; run <= target; b0 += NTQ) {
-        u = b0 + t < B ? seq_of(A, b0 + t).units : 0;
-        inc = run + block_inclusive(P, u, chunk);
-        if (target >= inc - u && target < inc) { P.b = b0 + t; P.pre = inc - u; }
+    long long run = 0;
+    for (int b0 = 0;;) {
+        if (target >= inc - u && target < inc) { P.b = b0 + t; P.kv = s.kv; P.n = s.n; P.pre = inc - u; }
         run += chunk;
+        b0 += NTQ;
+        if (run > target) break;                           // the same in every lane
+        s.units = 0;
+        if (b0 + t < B) s = seq_of(A, b0 + t);
+        u = static_cast<unsigned>(s.units);
+        inc = run + block_inclusive(P, u, chunk);
     }
     __syncthreads();
-    b = P.b;
-    pre = P.pre;
+    b = uniform(P.b);
+    kv = uniform(P.kv);
+    n = uniform(P.n);
+    pre = uniform(P.pre);
     return r;
 }
 
@@ -428,38 +472,59 @@ struct TileShape {
     static constexpr int RPI = 64 / CPR;                   // rows one load instruction of a wave fills
     static constexpr int RPI_SHIFT = RPI == 16 ? 4 : RPI == 8 ? 3 : RPI == 4 ? 2 : 1;
     static constexpr int NL = TT / RPI;                    // load instructions per tile
-    static constexpr int KB = TT * RB;                     // bytes of a tile
-    static constexpr int STAGE = NWQ * 2 * KB;             // keys and values of every wave's tile
-    // Row r's chunk c sits at place c ^ swz(r), so that the 16 lanes that read one
-    // chunk of 16 consecutive rows touch 16 different 16-byte columns of the banks.
-    __device__ static inline int swz(int r) {
-        return CPR >= 16 ? r & 15 : CPR == 8 ? (r >> 1) & 7 : (r >> 2) & 3;
-    }
+    // In LDS the rows of one load instruction are contiguous (1 KB), with PAD bytes between
+    // instructions, and row r's 16-byte chunk c is at place c ^ mix(r % RPI) of its row. So
+    // the 16 lanes that read one chunk of 16 consecutive rows touch 16 different 16-byte
+    // columns of the banks, and a lane's addresses for other chunks, rows 16 further
+    // on, and other load instructions differ by constants (the instructions' offsets).
+    static constexpr int PAD = CPR == 32 ? 32 : CPR == 4 ? 0 : 64;
+    static constexpr int GAP = 1024 + PAD;
+    __device__ static inline int mix(int lrow) { return CPR >= 16 ? lrow : CPR == 8 ? lrow >> 1 : lrow >> 2; }
+    __device__ static inline int place(int row) { return row / RPI * GAP + row % RPI * RB; }
+    static constexpr int NEXT16 = 16 / RPI * GAP;          // from row r to row r + 16
+    // Column blocks of the values whose addresses differ by more than constants.
+    static constexpr int AV = E4M3 ? 4 : CPR == 32 ? 1 : 2;
 };
 
-// Workgroups per CU (waves per SIMD): as many as LDS and the registers allow: the
-// accumulators, the queries, scores and weights, one tile's operands and about 70 more.
-constexpr int LDS_CU = 160 * 1024, LDS_MORE = 3 * 1024;    // per CU; a workgroup's beside the tiles
-template <int D, int MT, bool E4M3>
-constexpr int attn_occupancy() {
-    constexpr int lds = LDS_CU / (TileShape<D, E4M3>::STAGE + LDS_MORE);
-    constexpr int regs = 512 / (D * MT / 4 + D * MT / 8 + 12 * MT + D / (E4M3 ? 8 : 4) + 70);
-    return lds < regs ? lds : regs < 4 ? regs < 1 ? 1 : regs : 4;
-}
-// Tiles of a wave in LDS: the more loads in flight, the nearer to HBM's rate.
-template <int D, int MT, bool E4M3>
-constexpr int attn_stages() {
-    constexpr int n = (LDS_CU / attn_occupancy<D, MT, E4M3>() - LDS_MORE) / TileShape<D, E4M3>::STAGE;
-    return n < 1 ? 1 : n > 4 ? 4 : n;
-}
-
-template <class T, int D, int MT, bool E4M3>
-__global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_kernel(AttnParams A) {
+// How a workgroup's waves share the work. KEYS: each takes other keys, with all the query
+// rows (up to 32). ROWS, for more query rows: each takes other rows, MT * 16 of them, and
+// all walk the same tiles, which they load together; one barrier a tile.
+template <int D, int MT, bool E4M3, bool ROWS>
+struct AttnShape : TileShape<D, E4M3> {
     using S = TileShape<D, E4M3>;
-    constexpr int M16 = 16 * MT, ND = D / 16, NC = D / 32;
-    constexpr int NS = attn_stages<D, MT, E4M3>();
+    static constexpr int SUB = ROWS && S::NL < NWQ ? NWQ / S::NL : 1;      // steps of 32 keys a tile holds
+    static constexpr int KT = TT * SUB;                    // keys of a tile
+    static constexpr int NLW = ROWS ? S::NL * SUB / NWQ : S::NL;           // a wave's loads for its keys
+    static constexpr int HALF = KT / S::RPI * S::GAP;      // bytes of a tile's keys (or values)
+    static constexpr int STAGE = (ROWS ? 2 : 2 * NWQ) * HALF;              // of one tile (or one per wave)
+    static constexpr int M16 = 16 * MT * (ROWS ? NWQ : 1); // query rows
+    static constexpr int PARTS = ROWS ? 1 : NWQ;           // partial results per query row
+    // Workgroups per CU (waves per SIMD): as many as LDS and the registers allow: the
+    // accumulators, the queries, scores and weights, one tile's operands and about 70
+    // more (REST; with 90 at D = 64, where 128 registers spill a few: R * G = 1, 32 x 2047
+    // keys, 83 us at four waves to a SIMD, 73 at three). Then as many tiles in LDS as fit: the more loads in flight, the nearer to
+    // HBM's rate. With ROWS one tile is not in flight but in use.
+    static constexpr int LDS_CU = 160 * 1024, MORE = 4 * 1024;             // per CU; beside the tiles
+    static constexpr int REST = D == 64 && !E4M3 ? 90 : D == 128 && !ROWS && MT == 3 ? 50 : 70;
+    static constexpr int REGS = 512 / (D * MT / 4 + D * MT / 8 + 12 * MT + D / (E4M3 ? 8 : 4) + REST);
+    static constexpr int fit(int occ) { return (LDS_CU / occ - MORE) / STAGE; }
+    static constexpr int occupancy() {
+        int occ = REGS < 1 ? 1 : REGS > (ROWS ? 3 : 4) ? (ROWS ? 3 : 4) : REGS;
+        while (occ > 1 && fit(occ) < (ROWS ? 3 : 1)) --occ;
+        return occ;
+    }
+    static constexpr int OCC = occupancy();
+    static constexpr int NS = fit(OCC) > (ROWS ? 6 : 4) ? (ROWS ? 6 : 4) : fit(OCC);
+    static_assert(NS >= (ROWS ? 2 : 1) && (2 * NS - 1) * NLW <= 63, "tiles");
+};
+
+template <class T, int D, int MT, bool E4M3, bool ROWS>
+__global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn_kernel(AttnParams A) {
+    using S = AttnShape<D, MT, E4M3, ROWS>;
+    constexpr int M16 = S::M16, ND = D / 16, NC = D / 32, NS = S::NS, NP = S::PARTS, KT = S::KT;
+    constexpr int STRIDE = ROWS ? 1 : NWQ;                 // from a wave's tile to its next
     __shared__ __attribute__((aligned(16))) unsigned char lds[NS * S::STAGE];
-    __shared__ float st_m[NWQ][M16], st_l[NWQ][M16], fin[M16];
+    __shared__ float st_m[NP][M16], st_l[NP][M16], fin[M16];
     __shared__ Plan plan;
     __shared__ int odd_any;                                // some edge value was not finite
     const Cache& C = A.c;
@@ -471,9 +536,10 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
     if (x >= A.W * C.Hkv) return;
     const int h = x % C.Hkv, w = x / C.Hkv;
     if (t == 0) odd_any = 0;
-    int b = 0;
+    __syncthreads();
+    int b = 0, next_kv = 0, next_n = 0;
     long long pre = 0;
-    const Ranges ranges = locate(A, plan, w, b, pre);
+    const Ranges ranges = locate(A, plan, w, b, next_kv, next_n, pre);
     RangeRec* recs = reinterpret_cast<RangeRec*>(A.ws);
     const bool scribe = A.W > 1 && h == 0 && mb == 0 && t == 0;
     if (w >= ranges.ranges) {
@@ -483,18 +549,26 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
     long long at = ranges.start(w);
     const long long end = ranges.start(w + 1);
     bool first = true;
-
-
-    unsigned char* tiles_at = lds + wv * (NS * 2 * S::KB); // [stage][keys, values]
+    unsigned char* tiles_at = lds + (ROWS ? 0 : wv * (NS * 2 * S::HALF));  // [stage][keys, values]
     const char* kbase = C.k + h * C.ks[1];
     const char* vbase = C.v + h * C.vs[1];
     const float ksc = E4M3 ? C.k_scale[h] : 1.0f, vsc = E4M3 ? C.v_scale[h] : 1.0f;
     const float scale = A.scale * ksc;
     const int slot_mask = (1 << C.shift) - 1;
-    const int m0 = mb * M16;
+    // where this lane reads its operands in a tile: key r16, and (transposed) the piece of
+    // the values that it fetches for its group
+    const int k_at = S::place(r16) + (g ^ S::mix(r16 % S::RPI)) * 16;
+    int v_at[S::AV];
+#pragma unroll
+    for (int i = 0; i < S::AV; ++i) {
+        const int rr = r16 >> 1, row = !E4M3 ? 4 * g + (r16 >> 2) : rr < 4 ? 4 * g + rr : 12 + 4 * g + rr;
+        const int chunk = E4M3 ? i : 2 * i + (rr & 1);
+        v_at[i] = S::place(row) + (chunk ^ S::mix(row % S::RPI)) * 16 + (r16 & 1) * 8;
+    }
+    const int m0 = mb * M16, mw = ROWS ? wv * 16 * MT : 0; // the block's and, in it, the wave's first row
 
     while (at < end) {
-        const Seq sq = seq_of(A, b);
+        const Seq sq = first ? seq_from(A, next_kv, next_n) : seq_of(A, b);
         // the same in every lane: scalars
         const int kv = __builtin_amdgcn_readfirstlane(sq.kv), n_tok = __builtin_amdgcn_readfirstlane(sq.n);
         const int lo = __builtin_amdgcn_readfirstlane(sq.lo), hi = __builtin_amdgcn_readfirstlane(sq.hi);
@@ -519,14 +593,14 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
         }
         const bool whole = u0 == 0 && u1 == units;
         const int beg = base + u0 * TU, stop = min(hi, base + u1 * TU);
-        const int tiles = (stop - beg + TT - 1) / TT;
+        const int tiles = (stop - beg + KT - 1) / KT;
         const int* table = C.table + static_cast<long long>(b) * C.max_pages;
         int bad = 0;
-        // the page of key tile * TT + lane % 32 of the range; keys nobody sees are
-        // taken from the nearest that somebody does (and masked)
-        auto key_of = [&](int tile, int row) { return min(max(beg + tile * TT + row, lo), hi - 1); };
-        auto page_of = [&](int tile) {
-            int p = table[key_of(tile, lane & (TT - 1)) >> C.shift];
+        // the page of the tile's key lane % KT; keys nobody sees are taken from the
+        // nearest that somebody does (and masked)
+        auto key_of = [&](int tile, int row) { return min(max(beg + tile * KT + row, lo), hi - 1); };
+        auto page_at = [&](int tile) { return table[key_of(tile, lane & (KT - 1)) >> C.shift]; };
+        auto checked = [&](int p) {
             if (!page_ok(C, p)) { bad = 1; p = 0; }
             return p;
         };
@@ -534,40 +608,47 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
         // unless pages are shorter, so page and place are scalars; rows of keys nobody
         // sees then stand in a page that somebody needs.
         auto issue = [&](unsigned char* dst, const char* cache, const long long (&str)[3], int tile, int pages) {
+            const int j0 = ROWS ? wv * S::NLW : 0;
+            const int lrow = lane / S::CPR;
+            const unsigned off = static_cast<unsigned>(lrow) * static_cast<unsigned>(str[2]) +
+                                 static_cast<unsigned>((lane % S::CPR) ^ S::mix(lrow)) * 16u;
             if (C.shift >= S::RPI_SHIFT) {
-                const int lrow = opaque(lane / S::CPR);
-                const unsigned row_off = static_cast<unsigned>(lrow) * static_cast<unsigned>(str[2]);
 #pragma unroll
-                for (int j = 0; j < S::NL; ++j) {
-                    const int page = __builtin_amdgcn_readlane(pages, j * S::RPI);
-                    const int slot = (beg + tile * TT + j * S::RPI) & slot_mask;
+                for (int j = 0; j < S::NLW; ++j) {
+                    const int row = (j0 + j) * S::RPI;
+                    const int page = __builtin_amdgcn_readlane(pages, row);
+                    const int slot = (beg + tile * KT + row) & slot_mask;
                     const char* src = cache + page * str[0] + slot * str[2];
-                    const unsigned off = row_off + static_cast<unsigned>((lane % S::CPR) ^ S::swz(j * S::RPI + lrow)) * 16u;
-                    __builtin_amdgcn_global_load_lds((glb_ptr)(src + off), untraced((lds_ptr)(dst + j * 1024)), 16, 0, NT_LOAD);
+                    __builtin_amdgcn_global_load_lds((glb_ptr)(src + off), untraced((lds_ptr)(dst + (j0 + j) * S::GAP)),
+                                                     16, 0, NT_LOAD);
                 }
             } else {
 #pragma unroll 1
-                for (int j = 0; j < S::NL; ++j) {
-                    const int row = j * S::RPI + lane / S::CPR;
+                for (int j = j0; j < j0 + S::NLW; ++j) {
+                    const int row = j * S::RPI + lrow;
                     const int page = __shfl(pages, row, 64);
                     const int slot = key_of(tile, row) & slot_mask;
-                    const int chunk = (lane % S::CPR) ^ S::swz(row);
-                    const char* src = cache + page * str[0] + slot * str[2] + chunk * 16;
-                    __builtin_amdgcn_global_load_lds((glb_ptr)src, untraced((lds_ptr)(dst + j * 1024)), 16, 0, NT_LOAD);
+                    const char* src = cache + page * str[0] + slot * str[2] + ((lane % S::CPR) ^ S::mix(lrow)) * 16;
+                    __builtin_amdgcn_global_load_lds((glb_ptr)src, untraced((lds_ptr)(dst + j * S::GAP)), 16, 0, NT_LOAD);
                 }
             }
         };
-        int tile = wv, stage = 0;
-        int pages = 0;                                     // of the next tile to load
+        // the first tiles (all but one of the places with ROWS), and the next one's pages
+        constexpr int AHEAD = ROWS ? NS - 1 : NS;
+        int tile = ROWS ? 0 : wv, stage = 0;
+        int pages = 0;
         if (tile < tiles) {
+            int p[AHEAD + 1];
 #pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                if (tile + j * NWQ >= tiles) break;
-                const int now = page_of(tile + j * NWQ);
-                issue(tiles_at + j * 2 * S::KB, kbase, C.ks, tile + j * NWQ, now);
-                issue(tiles_at + j * 2 * S::KB + S::KB, vbase, C.vs, tile + j * NWQ, now);
+            for (int j = 0; j <= AHEAD; ++j) p[j] = page_at(tile + j * STRIDE);    // (past the last tile: the last key's)
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                if (tile + j * STRIDE >= tiles) break;
+                const int now = checked(p[j]);
+                issue(tiles_at + j * 2 * S::HALF, kbase, C.ks, tile + j * STRIDE, now);
+                issue(tiles_at + j * 2 * S::HALF + S::HALF, vbase, C.vs, tile + j * STRIDE, now);
             }
-            pages = page_of(tile + NS * NWQ);              // (past the last tile: the last key's)
+            pages = checked(p[AHEAD]);
         }
         // this lane's query rows: the MFMA's B operand, and where each one stands
         i32x4 qf[MT][NC];
@@ -575,7 +656,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
         float slope[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const int m = m0 + mt * 16 + r16;
+            const int m = m0 + mw + mt * 16 + r16;
             const int i = m < A.M ? m / A.G : 0, hq = h * A.G + (m < A.M ? m % A.G : 0);
             const char* row = A.q + b * A.qs[0] + i * A.qs[1] + hq * A.qs[2];
 #pragma unroll
@@ -597,28 +678,66 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
 #pragma unroll
             for (int d = 0; d < ND; ++d) acc[d][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        // One tile; MORE: NS tiles on the wave has another, loaded into this one's place as
-        // soon as its operands are read. Loads in flight are counted in their order: keys
-        // and values of a tile, then of the next.
+        // A weight of zero does not cancel a value that is not finite. Values that nobody sees
+        // become zeros; of those that only some rows see what is not finite does, and is
+        // added to the rows that see it at the end.
+        auto clean = [&](unsigned char* vt, int tok0, int from, int by) {
+            for (int c = from; c < KT * S::CPR; c += by) {
+                i32x4* at16 = reinterpret_cast<i32x4*>(vt + c / 64 * S::GAP + c % 64 * 16);
+                const int key = tok0 + c / S::CPR;
+                if (key < lo || key >= hi) {
+                    *at16 = i32x4{0, 0, 0, 0};
+                } else if (key > kv || (A.window > 0 && key <= hi - 1 - A.window)) {
+                    i32x4 v = *at16;
+                    if (strip<T, E4M3>(v)) { *at16 = v; odd_any = 1; }
+                }
+            }
+        };
+        // One tile; MORE: AHEAD tiles on there is another. Loads in flight are counted in
+        // their order: keys and values of a tile, then of the next. KEYS loads the other
+        // tile into this one's place as soon as the operands are read. ROWS loads it into
+        // the place of the tile before this one, which everyone is done with at the barrier.
         auto step = [&](auto MORE) {
             constexpr bool more = decltype(MORE)::value != 0;
-            unsigned char* kt = tiles_at + (NS > 1 ? stage : 0) * 2 * S::KB;
-            unsigned char* vt = kt + S::KB;
-            const int tok = beg + tile * TT, ro = opaque(r16), go = opaque(g);
-            wait_loads<(more ? (2 * NS - 1) * S::NL : NS > 1 ? 0 : S::NL)>();      // the keys are in
+            unsigned char* kt = tiles_at + (NS > 1 ? stage : 0) * 2 * S::HALF;
+            unsigned char* vt = kt + S::HALF;
+            const int tok0 = beg + tile * KT;
+            const int pages_now = pages;
+            if constexpr (ROWS) {
+                wait_loads<(more ? (NS - 2) * 2 * S::NLW : 0)>();
+                __syncthreads();
+                if constexpr (more) {
+                    unsigned char* to = tiles_at + (stage ? stage - 1 : NS - 1) * 2 * S::HALF;
+                    issue(to, kbase, C.ks, tile + AHEAD, pages_now);
+                    issue(to + S::HALF, vbase, C.vs, tile + AHEAD, pages_now);
+                    pages = checked(page_at(tile + AHEAD + 1));
+                }
+            } else {
+                wait_loads<(more ? (2 * NS - 1) * S::NLW : NS > 1 ? 0 : S::NLW)>();        // the keys are in
+            }
+            const bool edge = tok0 + KT - 1 > kv || (A.window > 0 && tok0 <= hi - 1 - A.window);
+            if (ROWS && edge) {
+                clean(vt, tok0, t, NTQ);
+                wait_lds();
+                __syncthreads();
+            }
+#pragma unroll
+            for (int sub = 0; sub < S::SUB; ++sub) {
+            const int tok = tok0 + sub * TT;
+            const unsigned char* kr = kt + k_at + sub * 2 * S::NEXT16;
+            unsigned char* vr = vt + sub * 2 * S::NEXT16;
             i32x4 kf[2][E4M3 ? NC / 2 : NC];
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                const int row = 16 * a + ro;
+            for (int a = 0; a < 2; ++a)
 #pragma unroll
                 for (int c = 0; c < (E4M3 ? NC / 2 : NC); ++c)
-                    kf[a][c] = *reinterpret_cast<const i32x4*>(kt + row * S::RB + ((c * 4 + go) ^ S::swz(row)) * 16);
-            }
-            wait_lds();                                    // their place is free
-            const int pages_now = pages;
-            if constexpr (more) {
-                issue(kt, kbase, C.ks, tile + NS * NWQ, pages_now);
-                pages = page_of(tile + (NS + 1) * NWQ);
+                    kf[a][c] = *reinterpret_cast<const i32x4*>(kr + a * S::NEXT16 + c * 64);
+            if constexpr (!ROWS) {
+                wait_lds();                                // their place is free
+                if constexpr (more) {
+                    issue(kt, kbase, C.ks, tile + NS * NWQ, pages_now);
+                    pages = checked(page_at(tile + (NS + 1) * NWQ));
+                }
             }
             f32x4 sc[2][MT];
 #pragma unroll
@@ -639,7 +758,6 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                 }
             }
             // scores in units of log2, masked
-            const bool edge = tok + TT - 1 > kv || (A.window > 0 && tok <= hi - 1 - A.window);
             if (A.softcap > 0.0f) {                        // cap tanh(v / cap) = cap (1 - 2 / (1 + e^(2 v / cap)))
                 const float c = A.softcap * LOG2E, e2 = scale / A.softcap * 2.0f * LOG2E;
 #pragma unroll
@@ -715,42 +833,31 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                     pf[mt][2 * a + 1] = static_cast<int>(pack2<T>(p[2], p[3]));
                 }
             }
-            wait_loads<(more ? (2 * NS - 1) * S::NL : 0)>();               // the values are in
-            if (edge) {
-                // A weight of zero does not cancel a value that is not finite. Values that
-                // nobody sees become zeros; of those that only some rows see what is not
-                // finite does, and is added to the rows that see it at the end.
-                for (int c = lane; c < TT * S::CPR; c += 64) {
-                    i32x4* at16 = reinterpret_cast<i32x4*>(vt + c * 16);
-                    const int key = tok + c / S::CPR;
-                    if (key < lo || key >= hi) {
-                        *at16 = i32x4{0, 0, 0, 0};
-                    } else if (key > kv || (A.window > 0 && key <= hi - 1 - A.window)) {
-                        i32x4 v = *at16;
-                        if (strip<T, E4M3>(v)) { *at16 = v; odd_any = 1; }
-                    }
+            if constexpr (!ROWS) {
+                wait_loads<(more ? (2 * NS - 1) * S::NLW : 0)>();          // the values are in
+                if (edge) {
+                    clean(vt, tok0, lane, 64);
+                    wait_lds();
                 }
-                wait_lds();
             }
             // columns 16 d .. 16 d + 15 of the values as the MFMA's A operand
             i32x2 vf[ND][E4M3 ? 1 : 2];
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
+                unsigned char* at_v = vr + v_at[d % S::AV] + d / S::AV * (S::AV * (E4M3 ? 16 : 32));
                 if constexpr (E4M3) {
-                    const int rr = ro >> 1, row = rr < 4 ? 4 * go + rr : 12 + 4 * go + rr;
-                    vf[d][0] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                        (lds_i32x2)(vt + row * S::RB + (d ^ S::swz(row)) * 16 + (ro & 1) * 8));
+                    vf[d][0] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2)at_v);
                 } else {
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        const int row = 16 * a + 4 * go + (ro >> 2), c = 2 * d + ((ro >> 1) & 1);
+                    for (int a = 0; a < 2; ++a)
                         vf[d][a] = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (lds_i16x4)(vt + row * S::RB + (c ^ S::swz(row)) * 16 + (ro & 1) * 8)));
-                    }
+                                                                 (lds_i16x4)(at_v + a * S::NEXT16)));
                 }
             }
-            wait_lds();                                    // their place is free
-            if constexpr (more) issue(vt, vbase, C.vs, tile + NS * NWQ, pages_now);
+            if constexpr (!ROWS) {
+                wait_lds();                                // their place is free
+                if constexpr (more) issue(vt, vbase, C.vs, tile + NS * NWQ, pages_now);
+            }
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
                 i32x4 v;
@@ -759,14 +866,15 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) acc[d][mt] = mfma<T>(v, pf[mt], acc[d][mt]);
             }
-            tile += NWQ;
+            }
+            tile += STRIDE;
             if (NS > 1) stage = stage + 1 < NS ? stage + 1 : 0;
         };
         if (tile < tiles) {
-            while (tile + NS * NWQ < tiles) step(Int<1>());
+            while (tile + AHEAD * STRIDE < tiles) step(Int<1>());
             do step(Int<0>()); while (tile < tiles);
         }
-        // ---- join the four waves
+        // ---- join the waves (KEYS), normalise, write
         const bool nan = __any(bad);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -775,8 +883,8 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
             l += __shfl_xor(l, 32, 64);
             if (nan) l = NAN;
             if (g == 0) {
-                st_m[wv][mt * 16 + r16] = mx[mt];
-                st_l[wv][mt * 16 + r16] = l;
+                st_m[ROWS ? 0 : wv][mw + mt * 16 + r16] = mx[mt];
+                st_l[ROWS ? 0 : wv][mw + mt * 16 + r16] = l;
             }
         }
         __syncthreads();                                   // the statistics are in, the tiles are free
@@ -785,17 +893,19 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                       (u0 == 0 ? M16 * (D + 2) : 0);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const int m = mt * 16 + r16;
-            float n = st_m[0][m];
+            const int m = mw + mt * 16 + r16;
+            float n = st_m[0][m], l = st_l[0][m];
+            if constexpr (!ROWS) {
 #pragma unroll
-            for (int j = 1; j < NWQ; ++j) n = fmaxf(n, st_m[j][m]);
-            float l = 0.0f;
+                for (int j = 1; j < NP; ++j) n = fmaxf(n, st_m[j][m]);
+                l = 0.0f;
 #pragma unroll
-            for (int j = 0; j < NWQ; ++j) l += st_l[j][m] * __builtin_amdgcn_exp2f(st_m[j][m] - n);
-            const float f = __builtin_amdgcn_exp2f(mx[mt] - n);
+                for (int j = 0; j < NP; ++j) l += st_l[j][m] * __builtin_amdgcn_exp2f(st_m[j][m] - n);
+                const float f = __builtin_amdgcn_exp2f(mx[mt] - n);
 #pragma unroll
-            for (int d = 0; d < ND; ++d) acc[d][mt] *= f;
-            if (t < 16) {                                  // group 0 of wave 0
+                for (int d = 0; d < ND; ++d) acc[d][mt] *= f;
+            }
+            if (g == 0 && (ROWS || wv == 0)) {
                 fin[m] = l;
                 if (!whole) {
                     slot[M16 * D + 2 * m] = n;
@@ -803,25 +913,28 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                 }
             }
         }
-        constexpr int FIT = NS * S::STAGE / (NWQ * M16 * 64);      // 16-element column blocks that fit
+        // through LDS as [part][16-element column block][row][16]: the writes of a wave and the
+        // reads of consecutive threads are contiguous
+        constexpr int FIT = NS * S::STAGE / (NP * M16 * 64);       // column blocks that fit
         constexpr int DC = FIT >= ND ? ND : FIT >= 8 ? 8 : FIT >= 4 ? 4 : FIT >= 2 ? 2 : 1;
         static_assert(FIT >= 1, "exchange");
-        float* ex = reinterpret_cast<float*>(lds);         // [wave][M16][16 DC]
+        float* ex = reinterpret_cast<float*>(lds);
 #pragma unroll
         for (int d0 = 0; d0 < ND; d0 += DC) {
 #pragma unroll
             for (int d = 0; d < DC; ++d)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                    *reinterpret_cast<f32x4*>(ex + ((wv * M16 + mt * 16 + r16) * DC + d) * 16 + 4 * g) = acc[d0 + d][mt];
+                    *reinterpret_cast<f32x4*>(ex + (((ROWS ? 0 : wv) * DC + d) * M16 + mw + mt * 16 + r16) * 16 + 4 * g) =
+                        acc[d0 + d][mt];
             __syncthreads();
             if (t == 0) odd_any = 0;                       // (everyone has read it)
             for (int i = t; i < M16 * DC * 4; i += NTQ) {
-                const int m = i / (DC * 4), d = d0 * 16 + i % (DC * 4) * 4;
+                const int m = i / 4 % M16, block = d0 + i / (4 * M16), d = block * 16 + i % 4 * 4;
                 if (m0 + m >= A.M) continue;
                 f32x4 o = *reinterpret_cast<const f32x4*>(ex + 4 * i);
 #pragma unroll
-                for (int j = 1; j < NWQ; ++j) o += *reinterpret_cast<const f32x4*>(ex + j * M16 * DC * 16 + 4 * i);
+                for (int j = 1; j < NP; ++j) o += *reinterpret_cast<const f32x4*>(ex + j * M16 * DC * 16 + 4 * i);
                 if (odd) {
                     const int at_pos = kv + min((m0 + m) / A.G, n_tok - 1);
                     const int from = max(beg, lo), past = min(stop, hi), seen_by_all = hi - A.window;
@@ -852,7 +965,7 @@ __global__ __launch_bounds__(NTQ, (attn_occupancy<D, MT, E4M3>())) void attn_ker
                     const long long row = (static_cast<long long>(b) * C.R + tk) * A.Hq + hq;
                     *reinterpret_cast<u32x2*>(A.out + (row * D + d) * 2) = y;
                 } else {
-                    *reinterpret_cast<f32x4*>(slot + m * D + d) = o;
+                    *reinterpret_cast<f32x4*>(slot + (block * M16 + m) * 16 + i % 4 * 4) = o;
                 }
             }
             __syncthreads();
@@ -900,7 +1013,7 @@ __global__ __launch_bounds__(NTQ) void join_kernel(AttnParams A) {
                                     (w == wa ? size : 0);
                 pm[j] = slot[A.M16 * A.D + 2 * m];
                 pl[j] = slot[A.M16 * A.D + 2 * m + 1];
-                po[j] = *reinterpret_cast<const f32x4*>(slot + m * A.D + col * 4);
+                po[j] = *reinterpret_cast<const f32x4*>(slot + (col / 4 * A.M16 + m) * 16 + col % 4 * 4);
             }
         }
         float nn = n;
@@ -1221,61 +1334,93 @@ int check_cache(int dtype, int32_t B, int32_t R, int32_t max_R, int32_t Hkv, int
 
 // Row blocks, ranges and workspace of an attention call.
 struct AttnPlan {
-    int M, MB, MT, W;
+    int M, MB, MT, M16, W;
+    bool rows;                 // the waves share the query rows (else the keys)
     size_t slots_at, bytes;
 };
 
-int attn_occupancy_of(int D, int MT, bool e4m3) {
-#define SPEC_OCC(d) (e4m3 ? MT == 1 ? attn_occupancy<d, 1, true>() : MT == 2 ? attn_occupancy<d, 2, true>() :         \
-                     MT == 3 ? attn_occupancy<d, 3, true>() : attn_occupancy<d, 4, true>() :                          \
-                     MT == 1 ? attn_occupancy<d, 1, false>() : MT == 2 ? attn_occupancy<d, 2, false>() :              \
-                     MT == 3 ? attn_occupancy<d, 3, false>() : attn_occupancy<d, 4, false>())
-    return D == 64 ? SPEC_OCC(64) : D == 128 ? SPEC_OCC(128) : SPEC_OCC(256);
-#undef SPEC_OCC
+template <int D, bool E4M3>
+int attn_occupancy(bool rows, int MT) {
+    if constexpr (E4M3 && D < 256) {
+        if (!rows && MT == 3) return AttnShape<D, 3, E4M3, false>::OCC;
+    }
+    if (!rows) return MT == 1 ? AttnShape<D, 1, E4M3, false>::OCC : AttnShape<D, 2, E4M3, false>::OCC;
+    if constexpr (D < 256) {
+        if (MT == 3) return AttnShape<D, 3, E4M3, true>::OCC;
+    }
+    return MT == 1 ? AttnShape<D, 1, E4M3, true>::OCC : AttnShape<D, 2, E4M3, true>::OCC;
 }
 
 AttnPlan attn_plan(int B, int R, int Hq, int Hkv, int D, bool e4m3, int page_size, int max_pages) {
     AttnPlan p;
     p.M = R * (Hq / Hkv);
-    const int tiles = (p.M + 15) / 16, most = D == 256 ? 2 : 4;
-    p.MB = (tiles + most - 1) / most;
-    p.MT = (tiles + p.MB - 1) / p.MB;
+    const int tiles = (p.M + 15) / 16;
+    // Up to 32 query rows the waves take keys each, beyond that rows each: with 48 rows and
+    // more a wave's accumulators leave only one wave to a SIMD (R * G = 40, 16 rows of 8192
+    // keys, bfloat16: 83 us by rows, 99 by keys at two waves to a SIMD, with spills). The
+    // exception are 8-bit caches, which every wave widens for itself: by rows that is four
+    // times the work (R * G = 40, 131071 keys: 74 us by rows, 67 by keys).
+    p.rows = tiles > (e4m3 && D < 256 ? 3 : 2);
+    p.MB = 1;
+    p.MT = tiles;
+    if (p.rows) {
+        const int most = NWQ * (D == 256 ? 2 : 3);
+        p.MB = (tiles + most - 1) / most;
+        p.MT = (tiles + NWQ * p.MB - 1) / (NWQ * p.MB);
+    }
+    p.M16 = 16 * p.MT * (p.rows ? NWQ : 1);
     // one resident round, but no more ranges than there can be units
     const int lanes = Hkv * p.MB;
-    long long w = CUS * attn_occupancy_of(D, p.MT, e4m3) / lanes;
-    const long long units = B * ((static_cast<long long>(max_pages) * page_size + TT + TU - 1) / TU);
+    const int occ = D == 64 ? (e4m3 ? attn_occupancy<64, true>(p.rows, p.MT) : attn_occupancy<64, false>(p.rows, p.MT))
+                  : D == 128 ? (e4m3 ? attn_occupancy<128, true>(p.rows, p.MT) : attn_occupancy<128, false>(p.rows, p.MT))
+                             : (e4m3 ? attn_occupancy<256, true>(p.rows, p.MT) : attn_occupancy<256, false>(p.rows, p.MT));
+    long long w = CUS * occ / lanes;
+    const long long units = B * ((static_cast<long long>(max_pages) * page_size + 2 * TT + TU - 1) / TU);
     if (w > units) w = units;
     p.W = w < 1 ? 1 : static_cast<int>(w);
     p.slots_at = (p.W * sizeof(RangeRec) + 255) & ~static_cast<size_t>(255);
-    p.bytes = p.slots_at + static_cast<size_t>(lanes) * p.W * 2 * 16 * p.MT * (D + 2) * sizeof(float);
+    p.bytes = p.slots_at + static_cast<size_t>(lanes) * p.W * 2 * p.M16 * (D + 2) * sizeof(float);
     p.bytes = p.W == 1 ? 256 : (p.bytes + 255) & ~static_cast<size_t>(255);
     return p;
 }
 
 template <class T, int D, bool E4M3>
-void launch_attn_m(const AttnParams& A, int MT, unsigned grid, hipStream_t s) {
-    if (MT == 1) hipLaunchKernelGGL((attn_kernel<T, D, 1, E4M3>), dim3(grid), dim3(NTQ), 0, s, A);
-    else if (MT == 2) hipLaunchKernelGGL((attn_kernel<T, D, 2, E4M3>), dim3(grid), dim3(NTQ), 0, s, A);
-    if constexpr (D < 256) {
-        if (MT == 3) hipLaunchKernelGGL((attn_kernel<T, D, 3, E4M3>), dim3(grid), dim3(NTQ), 0, s, A);
-        else if (MT == 4) hipLaunchKernelGGL((attn_kernel<T, D, 4, E4M3>), dim3(grid), dim3(NTQ), 0, s, A);
+void launch_attn_m(const AttnParams& A, const AttnPlan& p, unsigned grid, hipStream_t s) {
+    if (!p.rows) {
+        if constexpr (E4M3 && D < 256) {
+            if (p.MT == 3) {
+                hipLaunchKernelGGL((attn_kernel<T, D, 3, E4M3, false>), dim3(grid), dim3(NTQ), 0, s, A);
+                return;
+            }
+        }
+        if (p.MT == 1) hipLaunchKernelGGL((attn_kernel<T, D, 1, E4M3, false>), dim3(grid), dim3(NTQ), 0, s, A);
+        else hipLaunchKernelGGL((attn_kernel<T, D, 2, E4M3, false>), dim3(grid), dim3(NTQ), 0, s, A);
+        return;
     }
+    if constexpr (D < 256) {
+        if (p.MT == 3) {
+            hipLaunchKernelGGL((attn_kernel<T, D, 3, E4M3, true>), dim3(grid), dim3(NTQ), 0, s, A);
+            return;
+        }
+    }
+    if (p.MT == 1) hipLaunchKernelGGL((attn_kernel<T, D, 1, E4M3, true>), dim3(grid), dim3(NTQ), 0, s, A);
+    else hipLaunchKernelGGL((attn_kernel<T, D, 2, E4M3, true>), dim3(grid), dim3(NTQ), 0, s, A);
 }
 
 template <class T, int D>
-void launch_attn_d(const AttnParams& A, int MT, bool e4m3, unsigned grid, hipStream_t s) {
-    if (e4m3) launch_attn_m<T, D, true>(A, MT, grid, s);
-    else launch_attn_m<T, D, false>(A, MT, grid, s);
+void launch_attn_d(const AttnParams& A, const AttnPlan& p, bool e4m3, unsigned grid, hipStream_t s) {
+    if (e4m3) launch_attn_m<T, D, true>(A, p, grid, s);
+    else launch_attn_m<T, D, false>(A, p, grid, s);
 }
 
 template <class T>
-int launch_attn(AttnParams& A, int MT, bool e4m3, hipStream_t s) {
+int launch_attn(AttnParams& A, const AttnPlan& p, bool e4m3, hipStream_t s) {
     const long long x = static_cast<long long>(A.W) * A.c.Hkv;
     const long long grid = (x + 7) / 8 * 8 * A.MB;
     if (grid > (1ll << 31) - 1) return fail(SPEC_ERR_SHAPE, "R * Hq is too large");
-    if (A.D == 64) launch_attn_d<T, 64>(A, MT, e4m3, static_cast<unsigned>(grid), s);
-    else if (A.D == 128) launch_attn_d<T, 128>(A, MT, e4m3, static_cast<unsigned>(grid), s);
-    else launch_attn_d<T, 256>(A, MT, e4m3, static_cast<unsigned>(grid), s);
+    if (A.D == 64) launch_attn_d<T, 64>(A, p, e4m3, static_cast<unsigned>(grid), s);
+    else if (A.D == 128) launch_attn_d<T, 128>(A, p, e4m3, static_cast<unsigned>(grid), s);
+    else launch_attn_d<T, 256>(A, p, e4m3, static_cast<unsigned>(grid), s);
     const int rc = launched();
     if (rc != SPEC_OK || A.W == 1) return rc;              // one range: nothing crosses
     const int rows = NTQ / (A.D / 4) / A.slices, groups = (A.M16 + rows - 1) / rows;
@@ -1363,14 +1508,14 @@ int spec_attention(const void* q, const int64_t* q_stride, int dtype, int32_t B,
     A.ws = static_cast<float*>(workspace);
     A.scale = scale; A.softcap = softcap; A.window = window;
     A.Hq = Hq; A.G = Hq / Hkv; A.D = D;
-    A.M = plan.M; A.MB = plan.MB; A.M16 = 16 * plan.MT; A.W = plan.W;
+    A.M = plan.M; A.MB = plan.MB; A.M16 = plan.M16; A.W = plan.W;
     A.slots_at = static_cast<long long>(plan.slots_at / sizeof(float));
     A.direct = B < plan.W;
     // a sequence has about W / B pieces
     A.slices = 1;
     while (A.slices < NTQ / (D / 4) && A.slices * B < plan.W) A.slices *= 2;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    return dtype == SPEC_DTYPE_BF16 ? launch_attn<Bf16>(A, plan.MT, e4m3, s) : launch_attn<F16>(A, plan.MT, e4m3, s);
+    return dtype == SPEC_DTYPE_BF16 ? launch_attn<Bf16>(A, plan, e4m3, s) : launch_attn<F16>(A, plan, e4m3, s);
 }
 
 int spec_adjust(const void* logits, int32_t B, int32_t R, int32_t V, int dtype, const int32_t* draft_tokens, int32_t k,
