@@ -1059,20 +1059,26 @@ __global__ __launch_bounds__(NTQ) void join_kernel(AttnParams A) {
 
 // ------------------------------------------------------------------ logit adjustment
 //
-// Bound by memory: the logits are read and written once, the masks and the
-// histories are small beside them. A workgroup owns a segment of the
-// vocabulary for all R rows of a batch row. It counts the segment's tokens of
-// the history in LDS (integer atomics, so the order does not matter), streams
-// the segment of every row through registers with the mask applied, and then
-// goes over the few tokens with a count or a bias once more, taking their
-// logits from the input again and overwriting what it had stored. The streaming
-// part so has no lookups, and rows whose start is not 16-byte aligned (an odd
-// V) differ only in the head and tail elements that are moved one by one.
+// Bound by memory: the logits are read and written once, the masks and the histories are
+// small beside them. A workgroup owns a segment of the vocabulary for all R rows of a
+// batch row. It counts the segment's tokens of the history in LDS (integer atomics, so the
+// order does not matter), lists the few tokens with a count or a bias, streams the segment
+// of every row through registers with the mask applied, and then takes the listed tokens'
+// logits from the input again and overwrites what it had stored; the threads share list
+// and rows evenly, however the tokens cluster (one thread per token's place: 181 us
+// instead of .. at 64 x 6 x 151936, 2047 tokens of history). The streaming part so has no
+// lookups, and rows whose start is not 16-byte aligned (an odd V) differ only in the up to
+// 15 elements at the segment's ends that are moved one by one.
 
-constexpr int NTJ = 256;
-constexpr int SEG_MAX = 8192;                              // most tokens of a segment
+constexpr int NTJ = 512;
+constexpr int SEG_MAX = 6144;                              // most tokens of a segment: 24 KB of counts, 12 KB of list
+constexpr int SEG_MAX_BIAS = 3584;                         // ... with as many owners of biases beside them
+constexpr int SEG_MIN = 512;
+constexpr int ADJ_SLOTS = 4 * CUS;                         // resident workgroups
 constexpr unsigned SEEN = 0x80000000u;                     // count word: the token is in the prompt
+constexpr unsigned DRAFT = 0x40000000u;                    // ... or among the drafts
 constexpr unsigned NOBIAS = 0xffffffffu;
+constexpr int OPEN = -1, BROKEN = -2;                      // a row's mask: none; the row becomes NaN
 
 struct AdjustParams {
     const char* in;
@@ -1097,10 +1103,12 @@ struct AdjustParams {
 
 struct InF32 {
     static constexpr int VE = 4, ES = 4;
+    static constexpr unsigned NANS = 0x7fc00000u;
     __device__ static inline float one(const char* p, long long n) { return reinterpret_cast<const float*>(p)[n]; }
 };
 struct InBf16 {
     static constexpr int VE = 8, ES = 2;
+    static constexpr unsigned NANS = 0x7fc07fc0u;
     __device__ static inline float one(const char* p, long long n) {
         return bits_f32(static_cast<unsigned>(reinterpret_cast<const unsigned short*>(p)[n]) << 16);
     }
@@ -1154,13 +1162,16 @@ __device__ inline void put_vec(char* out, long long n, u32x4 w, unsigned bits) {
     }
 }
 
-template <class I, bool OF>
+template <class I, bool OF, bool BIAS>
 __global__ __launch_bounds__(NTJ) void adjust_kernel(AdjustParams A) {
-    __shared__ unsigned cnt[SEG_MAX], own[SEG_MAX];
-    __shared__ int dup;
+    constexpr int SEG = BIAS ? SEG_MAX_BIAS : SEG_MAX, VE = I::VE, U = 4;
+    __shared__ __attribute__((aligned(16))) unsigned cnt[SEG], own[BIAS ? SEG : 4];
+    __shared__ int mask_of[SPEC_MAX_K + 1], drafts[SPEC_MAX_K + 1];
+    __shared__ unsigned short list[SEG];
+    __shared__ int dup, listed;
     const int t = static_cast<int>(threadIdx.x);
     const int b = static_cast<int>(blockIdx.x) / A.nseg, s = static_cast<int>(blockIdx.x) % A.nseg;
-    const int v0 = s * A.seg, v1 = min(A.V, v0 + A.seg), len = v1 - v0;
+    const int v0 = s * A.seg, len = min(A.V - v0, A.seg);
     int rows = A.R;                                        // rows in use
     if (A.draft_len) {
         const int kb = A.draft_len[b];
@@ -1172,91 +1183,174 @@ __global__ __launch_bounds__(NTJ) void adjust_kernel(AdjustParams A) {
     const bool bad = n < 0 || n > A.H || p < 0 || p > n || !(rep > 0.0f && rep <= F32_MAX) ||
                      !(fabsf(freq) <= F32_MAX) || !(fabsf(pres) <= F32_MAX);
     const bool counts = (A.rep || A.freq || A.pres) && !bad;
-    const bool any = (counts && (n > 0 || A.k > 0)) || A.nb > 0;
+    const bool any = (counts && (n > 0 || A.k > 0)) || (BIAS && !bad);
+    const long long row0 = static_cast<long long>(b) * A.R;
+    if (t < rows) {
+        const int ar = A.admit ? (A.admit_row ? A.admit_row[row0 + t] : static_cast<int>(row0 + t)) : OPEN;
+        mask_of[t] = bad || ar < OPEN || (A.admit && ar >= A.n_admit) ? BROKEN : ar;
+    }
+    if (t < A.k)                                           // (0 .. len - 1: in the segment)
+        drafts[t] = static_cast<int>(static_cast<unsigned>(A.tokens[static_cast<long long>(b) * A.k + t]) -
+                                     static_cast<unsigned>(v0));
     if (any) {
-        for (int v = t; v < len; v += NTJ) { cnt[v] = 0; own[v] = NOBIAS; }
-        if (t == 0) dup = 0;
-        __syncthreads();
+        const u32x4 zero = {0, 0, 0, 0}, none = {NOBIAS, NOBIAS, NOBIAS, NOBIAS};
+        for (int v = 4 * t; v < len; v += 4 * NTJ) {
+            *reinterpret_cast<u32x4*>(cnt + v) = zero;
+            if constexpr (BIAS) *reinterpret_cast<u32x4*>(own + v) = none;
+        }
+        if (t == 0) dup = listed = 0;
+    }
+    __syncthreads();
+    if (any) {
         if (counts) {
             const int* h = A.history + static_cast<long long>(b) * A.H;
-            for (int j = t; j < n; j += NTJ) {
-                const unsigned v = static_cast<unsigned>(h[j]) - static_cast<unsigned>(v0);
+            auto count = [&](int token, int j) {
+                const unsigned v = static_cast<unsigned>(token) - static_cast<unsigned>(v0);
                 if (v < static_cast<unsigned>(len)) {
                     if (j < p) atomicOr(&cnt[v], SEEN);
                     else atomicAdd(&cnt[v], 1u);
                 }
+            };
+            // 16-byte loads, four in flight, between the unaligned ends
+            const int head = min(n, static_cast<int>(-(reinterpret_cast<uintptr_t>(h) / 4) & 3)), quads = (n - head) / 4;
+            for (int q0 = t; q0 < quads; q0 += U * NTJ) {
+                i32x4 v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int q = q0 + u * NTJ;
+                    v[u] = q < quads ? *reinterpret_cast<const i32x4*>(h + head + 4 * q) : i32x4{-1, -1, -1, -1};
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) count(v[u][j], head + 4 * (q0 + u * NTJ) + j);
+            }
+            if (t < head) count(h[t], t);
+            if (t < n - head - 4 * quads) count(h[head + 4 * quads + t], head + 4 * quads + t);
+            if (t < min(A.k, rows - 1) && static_cast<unsigned>(drafts[t]) < static_cast<unsigned>(len))
+                atomicOr(&cnt[drafts[t]], DRAFT);
+        }
+        if constexpr (BIAS) {
+            // the first entry of a biased token owns it; further ones are rare
+            for (int j = t; j < A.nb; j += NTJ) {
+                const unsigned v = static_cast<unsigned>(A.bias_tok[static_cast<long long>(b) * A.nb + j]) -
+                                   static_cast<unsigned>(v0);
+                if (v < static_cast<unsigned>(len) && atomicMin(&own[v], static_cast<unsigned>(j)) != NOBIAS) dup = 1;
             }
         }
-        // the first entry of a biased token owns it; further ones are rare
-        for (int j = t; j < A.nb; j += NTJ) {
-            const unsigned v = static_cast<unsigned>(A.bias_tok[static_cast<long long>(b) * A.nb + j]) -
-                               static_cast<unsigned>(v0);
-            if (v < static_cast<unsigned>(len) && atomicMin(&own[v], static_cast<unsigned>(j)) != NOBIAS) dup = 1;
-        }
-    }
-    // stream
-    for (int i = 0; i < rows; ++i) {
-        const long long row = static_cast<long long>(b) * A.R + i, n0 = row * A.V;
-        int ar = A.admit ? (A.admit_row ? A.admit_row[row] : static_cast<int>(row)) : -1;
-        if (bad || ar < -1 || (A.admit && ar >= A.n_admit)) {
-            for (int v = v0 + t; v < v1; v += NTJ) put_one<I, OF>(A.out, n0 + v, NAN);
-            continue;
-        }
-        const unsigned char* mask =
-            ar >= 0 ? reinterpret_cast<const unsigned char*>(A.admit + static_cast<long long>(ar) * A.W) : nullptr;
-        if (A.inplace && !mask) continue;                  // nothing to change
-        const int head = A.vec ? min(len, static_cast<int>(-(n0 + v0) & (I::VE - 1))) : len;
-        const int nvec = (len - head) / I::VE, tail = len - head - nvec * I::VE;
-        for (int q = t; q < nvec; q += NTJ) {
-            const int v = v0 + head + q * I::VE;
-            const u32x4 w = *reinterpret_cast<const u32x4*>(A.in + (n0 + v) * I::ES);
-            if (mask) put_vec<I, OF, true>(A.out, n0 + v, w, admit_bits<I::VE>(mask, v));
-            else put_vec<I, OF, false>(A.out, n0 + v, w, 0);
-        }
-        for (int q = t; q < head + tail; q += NTJ) {
-            const int v = q < head ? v0 + q : v1 - tail + (q - head);
-            const bool ok = !mask || (mask[v >> 3] >> (v & 7) & 1);
-            put_one<I, OF>(A.out, n0 + v, ok ? I::one(A.in, n0 + v) : -INFINITY);
-        }
-    }
-    if (!any || bad) return;
-    __builtin_amdgcn_s_waitcnt(0);                         // the stores above land before those below
-    __syncthreads();
-    // the tokens with a count or a bias
-    const int* tok = A.tokens + static_cast<long long>(b) * A.k;
-    if (counts) {
-        // drafts without a count of their own yet: mark them so that they are visited
-        for (int j = t; j < min(A.k, rows - 1); j += NTJ) {
-            const unsigned v = static_cast<unsigned>(tok[j]) - static_cast<unsigned>(v0);
-            if (v < static_cast<unsigned>(len)) atomicOr(&cnt[v], 0x40000000u);
+        __syncthreads();
+        for (int v4 = 4 * t; v4 < len; v4 += 4 * NTJ) {
+            const u32x4 c4 = *reinterpret_cast<const u32x4*>(cnt + v4);
+            u32x4 o4 = {NOBIAS, NOBIAS, NOBIAS, NOBIAS};
+            if constexpr (BIAS) o4 = *reinterpret_cast<const u32x4*>(own + v4);
+            if ((c4.x | c4.y | c4.z | c4.w) == 0 && (o4.x & o4.y & o4.z & o4.w) == NOBIAS) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (v4 + j < len && (c4[j] != 0 || o4[j] != NOBIAS))
+                    list[atomicAdd(&listed, 1)] = static_cast<unsigned short>(v4 + j);
         }
         __syncthreads();
     }
-    for (int v = t; v < len; v += NTJ) {
-        const unsigned c = cnt[v], o = own[v];
-        if (c == 0 && o == NOBIAS) continue;
-        const unsigned long long bo = static_cast<unsigned long long>(b) * A.nb;
-        float bias = 0.0f;
-        if (o != NOBIAS) {
-            bias = A.bias_val[bo + o];
-            if (dup)
-                for (int j = static_cast<int>(o) + 1; j < A.nb; ++j)
-                    if (A.bias_tok[bo + j] == v0 + v) bias += A.bias_val[bo + j];
+    const int active = any ? listed : 0;
+    // stream: item e is 16-byte vector e % nv of row e / nv, U of them in flight per thread
+    const unsigned char* admit = reinterpret_cast<const unsigned char*>(A.admit);
+    auto stored = [&](int m) { return !(A.inplace && m == OPEN); };        // else there is nothing to change
+    if (A.vec) {
+        const int nv = len / VE, items = rows * nv;
+        const float inv = 1.0f / static_cast<float>(max(nv, 1));
+        for (int e0 = t; e0 < items; e0 += U * NTJ) {
+            u32x4 x[U];
+            unsigned bits[U];
+            long long at[U];
+            int m[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int e = e0 + u * NTJ;
+                // exact: (e + 1/2) / nv is at least 1 / (2 nv) from an integer, and e < 2^18
+                const int i = static_cast<int>((static_cast<float>(e) + 0.5f) * inv), q = e - i * nv;
+                at[u] = -1;
+                m[u] = OPEN;
+                bits[u] = 0;
+                x[u] = u32x4{0, 0, 0, 0};
+                if (e < items) {
+                    const long long n0 = (row0 + i) * A.V + v0;
+                    const int head = static_cast<int>(-n0 & (VE - 1)), v = head + q * VE;
+                    m[u] = mask_of[i];
+                    if (v + VE <= len && stored(m[u])) {
+                        at[u] = n0 + v;
+                        x[u] = *reinterpret_cast<const u32x4*>(A.in + at[u] * I::ES);
+                        if (m[u] >= 0) bits[u] = admit_bits<VE>(admit + static_cast<long long>(m[u]) * (4ll * A.W), v0 + v);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (at[u] < 0) continue;
+                if (m[u] >= 0) put_vec<I, OF, true>(A.out, at[u], x[u], bits[u]);
+                else if (m[u] == OPEN) put_vec<I, OF, false>(A.out, at[u], x[u], 0);
+                else put_vec<I, OF, false>(A.out, at[u], u32x4{I::NANS, I::NANS, I::NANS, I::NANS}, 0);
+            }
         }
-        unsigned num = c & 0x3fffffffu;
-        bool seen = (c & SEEN) != 0 || num > 0;
-        for (int i = 0; i < rows; ++i) {
-            if (i > 0 && counts && tok[i - 1] == v0 + v) { ++num; seen = true; }
-            const long long row = static_cast<long long>(b) * A.R + i, at = row * A.V + v0 + v;
-            const int ar = A.admit ? (A.admit_row ? A.admit_row[row] : static_cast<int>(row)) : -1;
-            if (ar < -1 || (A.admit && ar >= A.n_admit)) continue;
-            if (ar >= 0 && !(A.admit[static_cast<long long>(ar) * A.W + ((v0 + v) >> 5)] >> ((v0 + v) & 31) & 1))
-                continue;
-            float x = I::one(A.in, at);
-            if (seen) x = x > 0.0f ? x / rep : x * rep;
-            if (num > 0) x = x - freq * static_cast<float>(num) - pres;
-            if (o != NOBIAS) x += bias;
-            put_one<I, OF>(A.out, at, x);
+    }
+    // the elements before and behind the vectors (all of them where the tensors are not
+    // 16-byte aligned)
+    const int ends = A.vec ? min(len, 2 * VE) : len;
+    for (int i = 0; i < rows; ++i) {
+        const int m = mask_of[i];
+        const long long n0 = (row0 + i) * A.V + v0;
+        const int head = A.vec ? min(len, static_cast<int>(-n0 & (VE - 1))) : len;
+        const int tail = (len - head) / VE * VE + head;    // the first behind the vectors
+        if (!stored(m)) continue;
+        for (int e = t; e < ends; e += NTJ) {
+            const int v = e < head ? e : tail + (e - head);
+            if (v >= len) break;
+            const bool ok = m < 0 || (admit[static_cast<long long>(m) * (4ll * A.W) + ((v0 + v) >> 3)] >> ((v0 + v) & 7) & 1);
+            put_one<I, OF>(A.out, n0 + v, m == BROKEN ? NAN : ok ? I::one(A.in, n0 + v) : -INFINITY);
+        }
+    }
+    if (active == 0) return;
+    __builtin_amdgcn_s_waitcnt(0);                         // the stores above land before those below
+    __syncthreads();
+    // the listed tokens: item e is entry e % active in row e / active
+    const unsigned long long bo = static_cast<unsigned long long>(b) * A.nb;
+    const int items = rows * active;
+    const float inv = 1.0f / static_cast<float>(active);
+    for (int e0 = t; e0 < items; e0 += U * NTJ) {
+        float x[U];
+        int v[U], row[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = e0 + u * NTJ;
+            row[u] = -1;
+            x[u] = 0.0f;
+            if (e >= items) continue;
+            const int i = static_cast<int>((static_cast<float>(e) + 0.5f) * inv);  // exact: e < 2^19
+            v[u] = list[e - i * active];
+            const int m = mask_of[i];
+            if (m == OPEN || (m >= 0 && (admit[static_cast<long long>(m) * (4ll * A.W) + ((v0 + v[u]) >> 3)] >>
+                                         ((v0 + v[u]) & 7) & 1))) {
+                row[u] = i;
+                x[u] = I::one(A.in, (row0 + i) * A.V + v0 + v[u]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (row[u] < 0) continue;
+            const unsigned c = cnt[v[u]], o = BIAS ? own[v[u]] : NOBIAS;
+            unsigned num = c & (DRAFT - 1);
+            if ((c & DRAFT) != 0)
+                for (int j = 0; j < row[u]; ++j) num += drafts[j] == v[u];
+            float y = x[u];
+            if ((c & SEEN) != 0 || num > 0) y = y > 0.0f ? y / rep : y * rep;
+            if (num > 0) y = y - freq * static_cast<float>(num) - pres;
+            if (o != NOBIAS) {
+                float bias = A.bias_val[bo + o];
+                if (dup)
+                    for (int j = static_cast<int>(o) + 1; j < A.nb; ++j)
+                        if (A.bias_tok[bo + j] == v0 + v[u]) bias += A.bias_val[bo + j];
+                y += bias;
+            }
+            put_one<I, OF>(A.out, (row0 + row[u]) * A.V + v0 + v[u], y);
         }
     }
 }
@@ -1429,6 +1523,16 @@ int launch_attn(AttnParams& A, const AttnPlan& p, bool e4m3, hipStream_t s) {
     return launched();
 }
 
+template <bool BIAS>
+void launch_adjust(const AdjustParams& A, int dtype, int out_dtype, unsigned grid, hipStream_t s) {
+    if (dtype == SPEC_DTYPE_F32)
+        hipLaunchKernelGGL((adjust_kernel<InF32, false, BIAS>), dim3(grid), dim3(NTJ), 0, s, A);
+    else if (out_dtype == SPEC_DTYPE_BF16)
+        hipLaunchKernelGGL((adjust_kernel<InBf16, false, BIAS>), dim3(grid), dim3(NTJ), 0, s, A);
+    else
+        hipLaunchKernelGGL((adjust_kernel<InBf16, true, BIAS>), dim3(grid), dim3(NTJ), 0, s, A);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1564,17 +1668,24 @@ int spec_adjust(const void* logits, int32_t B, int32_t R, int32_t V, int dtype, 
     A.W = (V + 31) / 32;
     A.vec = aligned(logits, 16) && aligned(out, 16);
     A.inplace = out == logits;
-    A.seg = 4096;
+    // Segments: as few as fit LDS, then as many more as fill the rounds of resident
+    // workgroups that these take, unless reading the history once more per segment would
+    // cost more than the logits do.
+    const int most = n_bias > 0 ? SEG_MAX_BIAS : SEG_MAX;
+    const long long least = (V + most - 1) / most;
+    const long long rounds = (B * least + ADJ_SLOTS - 1) / ADJ_SLOTS;
+    long long nseg = rounds * ADJ_SLOTS / B;
+    const long long line = static_cast<long long>(R) * V * static_cast<long long>(es + eo);
+    if (H > 0 && nseg > line / (4ll * H)) nseg = line / (4ll * H);
+    if (nseg > (V + SEG_MIN - 1) / SEG_MIN) nseg = (V + SEG_MIN - 1) / SEG_MIN;
+    if (nseg < least) nseg = least;
+    A.seg = static_cast<int>(((V + nseg - 1) / nseg + 63) / 64 * 64);
     A.nseg = (V + A.seg - 1) / A.seg;
     const long long grid = static_cast<long long>(B) * A.nseg;
     if (grid > (1ll << 31) - 1) return fail(SPEC_ERR_SHAPE, "B * V is too large");
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (dtype == SPEC_DTYPE_F32)
-        hipLaunchKernelGGL((adjust_kernel<InF32, false>), dim3(static_cast<unsigned>(grid)), dim3(NTJ), 0, s, A);
-    else if (out_dtype == SPEC_DTYPE_BF16)
-        hipLaunchKernelGGL((adjust_kernel<InBf16, false>), dim3(static_cast<unsigned>(grid)), dim3(NTJ), 0, s, A);
-    else
-        hipLaunchKernelGGL((adjust_kernel<InBf16, true>), dim3(static_cast<unsigned>(grid)), dim3(NTJ), 0, s, A);
+    if (n_bias > 0) launch_adjust<true>(A, dtype, out_dtype, static_cast<unsigned>(grid), s);
+    else launch_adjust<false>(A, dtype, out_dtype, static_cast<unsigned>(grid), s);
     return launched();
 }
 
