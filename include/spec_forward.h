@@ -136,7 +136,7 @@ size_t spec_attention_workspace_size(int32_t B, int32_t R, int32_t Hq, int32_t H
  * [-1, n_admit). With draft_len, rows behind the ones in use (the first k_b + 1 target
  * rows or k_b draft rows; a batch row whose draft_len is outside [0, k]: all) are left as
  * they were.
- * 1 <= B <= 2^21, 0 <= k <= SPEC_MAX_K, R >= 1, 1 <= V <= 2^29, 0 <= H <= 2^30 (0: no
+ * 1 <= B <= 2^21, 0 <= k <= SPEC_MAX_K, R >= 1, 1 <= V <= 2^29, 0 <= H < 2^29 (0: no
  * history), 0 <= n_bias <= 65536. Enqueues one kernel, no workspace. Errors:
  * SPEC_ERR_SHAPE, SPEC_ERR_DTYPE, SPEC_ERR_NULL, SPEC_ERR_ALIGN, SPEC_ERR_HIP.
  */

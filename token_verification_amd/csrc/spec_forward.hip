@@ -1063,21 +1063,23 @@ __global__ __launch_bounds__(NTQ) void join_kernel(AttnParams A) {
 // small beside them. A workgroup owns a segment of the vocabulary for all R rows of a
 // batch row. It counts the segment's tokens of the history in LDS (integer atomics, so the
 // order does not matter), lists the few tokens with a count or a bias, streams the segment
-// of every row through registers with the mask applied, and then takes the listed tokens'
-// logits from the input again and overwrites what it had stored; the threads share list
-// and rows evenly, however the tokens cluster (one thread per token's place: 181 us
-// instead of .. at 64 x 6 x 151936, 2047 tokens of history). The streaming part so has no
-// lookups, and rows whose start is not 16-byte aligned (an odd V) differ only in the up to
-// 15 elements at the segment's ends that are moved one by one.
+// of every row through registers with the mask applied, and overwrites the listed tokens,
+// whose logits it took before the stream. The streaming loop so has no lookups, and rows
+// whose start is not 16-byte aligned (an odd V) differ only in the up to 15 elements at
+// the segment's ends that are moved one by one. A segment with many such tokens (those of
+// a text cluster) is instead adjusted element by element in the stream.
 
 constexpr int NTJ = 512;
-constexpr int SEG_MAX = 6144;                              // most tokens of a segment: 24 KB of counts, 12 KB of list
-constexpr int SEG_MAX_BIAS = 3584;                         // ... with as many owners of biases beside them
+constexpr int SEG_MAX = 8192;                              // most tokens of a segment (32 KB of counts)
+constexpr int SEG_MAX_BIAS = 5120;                         // ... with as many 16-bit owners of biases beside them
 constexpr int SEG_MIN = 512;
 constexpr int ADJ_SLOTS = 4 * CUS;                         // resident workgroups
-constexpr unsigned SEEN = 0x80000000u;                     // count word: the token is in the prompt
-constexpr unsigned DRAFT = 0x40000000u;                    // ... or among the drafts
-constexpr unsigned NOBIAS = 0xffffffffu;
+constexpr int DENSE = 16;                                  // many: more than one token in 16
+// count word: the low bits count the token behind the prompt
+constexpr unsigned SEEN = 0x80000000u;                     // it is in the prompt
+constexpr unsigned DRAFT = 0x40000000u;                    // it is among the drafts
+constexpr unsigned BIASED = 0x20000000u;                   // it has a bias
+constexpr unsigned COUNT = BIASED - 1;
 constexpr int OPEN = -1, BROKEN = -2;                      // a row's mask: none; the row becomes NaN
 
 struct AdjustParams {
@@ -1121,31 +1123,59 @@ __device__ inline void put_one(char* p, long long n, float x) {
     else reinterpret_cast<__bf16*>(p)[n] = static_cast<__bf16>(x);
 }
 
-// the admit bits of tokens v..v+VE-1 (all < V) in the low bits
+// The admit bits of tokens v..v+VE-1 (all < V) in the low bits; `whole`: they never cross a byte.
 template <int VE>
-__device__ inline unsigned admit_bits(const unsigned char* row, int v) {
-    const unsigned lo = row[v >> 3], hi = row[(v + VE - 1) >> 3];
-    return (lo | hi << 8) >> (v & 7);
+__device__ inline unsigned admit_bits(const unsigned char* row, int v, bool whole) {
+    unsigned w = row[static_cast<unsigned>(v) >> 3];
+    if (!whole) w |= static_cast<unsigned>(row[static_cast<unsigned>(v + VE - 1) >> 3]) << 8;
+    return w >> (v & 7);
+}
+
+template <class I>
+__device__ inline void unpack(u32x4 w, float (&y)[I::VE]) {
+    if constexpr (I::ES == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = bits_f32(w[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { y[2 * j] = bits_f32(w[j] << 16); y[2 * j + 1] = bits_f32(w[j] & 0xffff0000u); }
+    }
+}
+
+template <class I, bool OF>
+__device__ inline void put_floats(char* out, const float (&y)[I::VE]) {
+    if constexpr (OF || I::ES == 4) {
+#pragma unroll
+        for (int j = 0; j < I::VE; j += 4)
+            reinterpret_cast<f32x4*>(out)[j / 4] = f32x4{y[j], y[j + 1], y[j + 2], y[j + 3]};
+    } else {
+        *reinterpret_cast<u32x4*>(out) = u32x4{pack2<Bf16>(y[0], y[1]), pack2<Bf16>(y[2], y[3]),
+                                               pack2<Bf16>(y[4], y[5]), pack2<Bf16>(y[6], y[7])};
+    }
+}
+
+// w where the mask's bits are set, else -infinity
+__device__ inline unsigned pick(unsigned mask, unsigned w, unsigned inf) { return (w & mask) | (inf & ~mask); }
+// all ones if bit j of bits is set, else zero
+__device__ inline unsigned spread(unsigned bits, int j) {
+    return static_cast<unsigned>(static_cast<int>(bits << (31 - j)) >> 31);
 }
 
 template <class I, bool OF, bool MASK>
-__device__ inline void put_vec(char* out, long long n, u32x4 w, unsigned bits) {
+__device__ inline void put_vec(char* out, u32x4 w, unsigned bits) {
     if constexpr (I::ES == 4) {
         if constexpr (MASK) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = (bits >> j) & 1 ? w[j] : 0xff800000u;
+            for (int j = 0; j < 4; ++j) w[j] = pick(spread(bits, j), w[j], 0xff800000u);
         }
-        *reinterpret_cast<u32x4*>(out + 4 * n) = w;
+        *reinterpret_cast<u32x4*>(out) = w;
     } else if constexpr (!OF) {
         if constexpr (MASK) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const unsigned lo = (bits >> (2 * j)) & 1 ? w[j] & 0xffffu : 0xff80u;
-                const unsigned hi = (bits >> (2 * j + 1)) & 1 ? w[j] & 0xffff0000u : 0xff800000u;
-                w[j] = lo | hi;
-            }
+            for (int j = 0; j < 4; ++j)
+                w[j] = pick((spread(bits, 2 * j) & 0xffffu) | (spread(bits, 2 * j + 1) & 0xffff0000u), w[j], 0xff80ff80u);
         }
-        *reinterpret_cast<u32x4*>(out + 2 * n) = w;
+        *reinterpret_cast<u32x4*>(out) = w;
     } else {
         u32x4 a, b;
         a.x = w.x << 16; a.y = w.x & 0xffff0000u; a.z = w.y << 16; a.w = w.y & 0xffff0000u;
@@ -1153,24 +1183,27 @@ __device__ inline void put_vec(char* out, long long n, u32x4 w, unsigned bits) {
         if constexpr (MASK) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                a[j] = (bits >> j) & 1 ? a[j] : 0xff800000u;
-                b[j] = (bits >> (4 + j)) & 1 ? b[j] : 0xff800000u;
+                a[j] = pick(spread(bits, j), a[j], 0xff800000u);
+                b[j] = pick(spread(bits, 4 + j), b[j], 0xff800000u);
             }
         }
-        *reinterpret_cast<u32x4*>(out + 4 * n) = a;
-        *reinterpret_cast<u32x4*>(out + 4 * n + 16) = b;
+        reinterpret_cast<u32x4*>(out)[0] = a;
+        reinterpret_cast<u32x4*>(out)[1] = b;
     }
 }
 
 template <class I, bool OF, bool BIAS>
-__global__ __launch_bounds__(NTJ) void adjust_kernel(AdjustParams A) {
+__global__ __launch_bounds__(NTJ, 8) void adjust_kernel(AdjustParams A) {
     constexpr int SEG = BIAS ? SEG_MAX_BIAS : SEG_MAX, VE = I::VE, U = 4;
-    __shared__ __attribute__((aligned(16))) unsigned cnt[SEG], own[BIAS ? SEG : 4];
+    __shared__ __attribute__((aligned(16))) unsigned cnt[SEG];
+    __shared__ unsigned short own[BIAS ? SEG : 1], list[SEG / DENSE];
     __shared__ int mask_of[SPEC_MAX_K + 1], drafts[SPEC_MAX_K + 1];
-    __shared__ unsigned short list[SEG];
     __shared__ int dup, listed;
     const int t = static_cast<int>(threadIdx.x);
-    const int b = static_cast<int>(blockIdx.x) / A.nseg, s = static_cast<int>(blockIdx.x) % A.nseg;
+    // Low segments first: vocabularies put frequent tokens there, so these take longest. Batch
+    // rows are rotated, so that the segments of one do not meet on one XCD and read its
+    // history through the same channels of that L2 at the same time.
+    const int s = static_cast<int>(blockIdx.x) / A.B, b = (static_cast<int>(blockIdx.x) % A.B + s) % A.B;
     const int v0 = s * A.seg, len = min(A.V - v0, A.seg);
     int rows = A.R;                                        // rows in use
     if (A.draft_len) {
@@ -1192,12 +1225,47 @@ __global__ __launch_bounds__(NTJ) void adjust_kernel(AdjustParams A) {
     if (t < A.k)                                           // (0 .. len - 1: in the segment)
         drafts[t] = static_cast<int>(static_cast<unsigned>(A.tokens[static_cast<long long>(b) * A.k + t]) -
                                      static_cast<unsigned>(v0));
-    if (any) {
-        const u32x4 zero = {0, 0, 0, 0}, none = {NOBIAS, NOBIAS, NOBIAS, NOBIAS};
-        for (int v = 4 * t; v < len; v += 4 * NTJ) {
-            *reinterpret_cast<u32x4*>(cnt + v) = zero;
-            if constexpr (BIAS) *reinterpret_cast<u32x4*>(own + v) = none;
+    // The stream's items are 64 consecutive 16-byte vectors of a row, one per lane, wave by
+    // wave: row, place and mask are scalars.
+    constexpr int EO = OF ? 4 : I::ES;
+    const int lane = t & 63, wv = uniform(t >> 6);
+    const int chunks = A.vec ? (len / VE + 63) / 64 : 0;
+    const bool whole = A.V % 8 == 0;
+    struct Item {
+        int row, chunk;
+    };
+    auto advance = [&](Item& it) {
+        it.chunk += NTJ / 64;
+        while (it.chunk >= chunks) { it.chunk -= chunks; ++it.row; }
+    };
+    auto row_at = [&](int row) { return (row0 + row) * A.V + v0; };
+    // the lane's first token; it has a vector if the VE tokens are in the segment
+    auto token = [&](const Item& it) {
+        return static_cast<int>(-row_at(it.row) & (VE - 1)) + (it.chunk * 64 + lane) * VE;
+    };
+    Item it0{0, wv - NTJ / 64};
+    if (chunks > 0) advance(it0);
+    else it0.row = rows;
+    auto load = [&](const Item& it) {                      // read once (or, where adjusted, just before)
+        const unsigned v = static_cast<unsigned>(token(it));
+        if (it.row >= rows || v + VE > static_cast<unsigned>(len)) return u32x4{0, 0, 0, 0};
+        return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(A.in + row_at(it.row) * I::ES + v * I::ES));
+    };
+    // the first items' logits come in while the history is counted
+    u32x4 x[U];
+    {
+        Item it = it0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            x[u] = u32x4{0, 0, 0, 0};
+            if (!A.inplace && chunks > 0) {
+                x[u] = load(it);
+                advance(it);
+            }
         }
+    }
+    if (any) {
+        for (int v = 4 * t; v < len; v += 4 * NTJ) *reinterpret_cast<u32x4*>(cnt + v) = u32x4{0, 0, 0, 0};
         if (t == 0) dup = listed = 0;
     }
     __syncthreads();
@@ -1231,126 +1299,136 @@ __global__ __launch_bounds__(NTJ) void adjust_kernel(AdjustParams A) {
                 atomicOr(&cnt[drafts[t]], DRAFT);
         }
         if constexpr (BIAS) {
-            // the first entry of a biased token owns it; further ones are rare
             for (int j = t; j < A.nb; j += NTJ) {
                 const unsigned v = static_cast<unsigned>(A.bias_tok[static_cast<long long>(b) * A.nb + j]) -
                                    static_cast<unsigned>(v0);
-                if (v < static_cast<unsigned>(len) && atomicMin(&own[v], static_cast<unsigned>(j)) != NOBIAS) dup = 1;
+                if (v < static_cast<unsigned>(len)) {
+                    if (atomicOr(&cnt[v], BIASED) & BIASED) dup = 1;       // a token twice in the list: rare
+                    else own[v] = static_cast<unsigned short>(j);
+                }
             }
         }
         __syncthreads();
         for (int v4 = 4 * t; v4 < len; v4 += 4 * NTJ) {
-            const u32x4 c4 = *reinterpret_cast<const u32x4*>(cnt + v4);
-            u32x4 o4 = {NOBIAS, NOBIAS, NOBIAS, NOBIAS};
-            if constexpr (BIAS) o4 = *reinterpret_cast<const u32x4*>(own + v4);
-            if ((c4.x | c4.y | c4.z | c4.w) == 0 && (o4.x & o4.y & o4.z & o4.w) == NOBIAS) continue;
+            const u32x4 c = *reinterpret_cast<const u32x4*>(cnt + v4);
+            if ((c.x | c.y | c.z | c.w) == 0) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (v4 + j < len && (c4[j] != 0 || o4[j] != NOBIAS))
-                    list[atomicAdd(&listed, 1)] = static_cast<unsigned short>(v4 + j);
+                if (c[j] != 0) {
+                    const int at = atomicAdd(&listed, 1);
+                    if (at < SEG / DENSE) list[at] = static_cast<unsigned short>(v4 + j);
+                }
         }
         __syncthreads();
     }
     const int active = any ? listed : 0;
-    // stream: item e is 16-byte vector e % nv of row e / nv, U of them in flight per thread
+    const bool dense = active > min(len, SEG) / DENSE;
+    const unsigned long long bo = static_cast<unsigned long long>(b) * A.nb;
     const unsigned char* admit = reinterpret_cast<const unsigned char*>(A.admit);
-    auto stored = [&](int m) { return !(A.inplace && m == OPEN); };        // else there is nothing to change
-    if (A.vec) {
-        const int nv = len / VE, items = rows * nv;
-        const float inv = 1.0f / static_cast<float>(max(nv, 1));
-        for (int e0 = t; e0 < items; e0 += U * NTJ) {
-            u32x4 x[U];
-            unsigned bits[U];
-            long long at[U];
-            int m[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int e = e0 + u * NTJ;
-                // exact: (e + 1/2) / nv is at least 1 / (2 nv) from an integer, and e < 2^18
-                const int i = static_cast<int>((static_cast<float>(e) + 0.5f) * inv), q = e - i * nv;
-                at[u] = -1;
-                m[u] = OPEN;
-                bits[u] = 0;
-                x[u] = u32x4{0, 0, 0, 0};
-                if (e < items) {
-                    const long long n0 = (row0 + i) * A.V + v0;
-                    const int head = static_cast<int>(-n0 & (VE - 1)), v = head + q * VE;
-                    m[u] = mask_of[i];
-                    if (v + VE <= len && stored(m[u])) {
-                        at[u] = n0 + v;
-                        x[u] = *reinterpret_cast<const u32x4*>(A.in + at[u] * I::ES);
-                        if (m[u] >= 0) bits[u] = admit_bits<VE>(admit + static_cast<long long>(m[u]) * (4ll * A.W), v0 + v);
-                    }
+    auto mask_row = [&](int m) { return admit + static_cast<long long>(m) * (4ll * A.W); };
+    // the adjusted logit of the segment's token v in row i
+    auto adjusted = [&](float y, int v, int i) {
+        const unsigned c = cnt[v];
+        unsigned num = c & COUNT;
+        if ((c & DRAFT) != 0)
+            for (int j = 0; j < i; ++j) num += drafts[j] == v;
+        if ((c & SEEN) != 0 || num > 0) y = y > 0.0f ? y / rep : y * rep;
+        if (num > 0) y = y - freq * static_cast<float>(num) - pres;
+        if constexpr (BIAS) {
+            if ((c & BIASED) != 0) {
+                if (!dup) {
+                    y += A.bias_val[bo + own[v]];
+                } else {
+                    float bias = 0.0f;
+                    for (int j = 0; j < A.nb; ++j)
+                        if (A.bias_tok[bo + j] == v0 + v) bias += A.bias_val[bo + j];
+                    y += bias;
                 }
             }
+        }
+        return y;
+    };
+    // the first U of a thread's listed tokens: entry e % active in row e / active
+    const int todo = dense ? 0 : rows * active;
+    const float share = 1.0f / static_cast<float>(max(active, 1));
+    auto entry = [&](int e, int& i, int& v) {
+        i = static_cast<int>((static_cast<float>(e) + 0.5f) * share);
+        v = e < todo ? list[e - i * active] : 0;
+        const int m = e < todo ? mask_of[i] : BROKEN;
+        return m == OPEN || (m >= 0 && (mask_row(m)[(v0 + v) >> 3] >> ((v0 + v) & 7) & 1));
+    };
+    float early[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (at[u] < 0) continue;
-                if (m[u] >= 0) put_vec<I, OF, true>(A.out, at[u], x[u], bits[u]);
-                else if (m[u] == OPEN) put_vec<I, OF, false>(A.out, at[u], x[u], 0);
-                else put_vec<I, OF, false>(A.out, at[u], u32x4{I::NANS, I::NANS, I::NANS, I::NANS}, 0);
+    for (int u = 0; u < U; ++u) {
+        int i, v;
+        early[u] = 0.0f;
+        if (t + u * NTJ < todo && entry(t + u * NTJ, i, v)) early[u] = I::one(A.in, (row0 + i) * A.V + v0 + v);
+    }
+    bool first = !A.inplace;
+    for (Item it = it0; it.row < rows; first = false) {
+        unsigned bits[U];
+        Item at[U];
+        int m[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            at[u] = it;
+            bits[u] = 0;
+            m[u] = OPEN;
+            if (it.row >= rows) continue;
+            m[u] = uniform(mask_of[it.row]);
+            if (!first && (!A.inplace || m[u] != OPEN || dense)) x[u] = load(it);
+            const int v = token(it);
+            if (m[u] >= 0 && v + VE <= len) bits[u] = admit_bits<VE>(mask_row(m[u]), v0 + v, whole);
+            advance(it);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = token(at[u]);
+            if (at[u].row >= rows || v + VE > len || (A.inplace && m[u] == OPEN && !dense)) continue;
+            char* out = A.out + row_at(at[u].row) * EO + static_cast<unsigned>(v) * EO;
+            if (m[u] == BROKEN) {
+                put_vec<I, OF, false>(out, u32x4{I::NANS, I::NANS, I::NANS, I::NANS}, 0);
+            } else if (dense) {
+                float y[VE];
+                unpack<I>(x[u], y);
+#pragma unroll
+                for (int j = 0; j < VE; ++j) {
+                    if (cnt[v + j] != 0) y[j] = adjusted(y[j], v + j, at[u].row);
+                    if (m[u] >= 0 && !((bits[u] >> j) & 1)) y[j] = -INFINITY;
+                }
+                put_floats<I, OF>(out, y);
+            } else if (m[u] >= 0) {
+                put_vec<I, OF, true>(out, x[u], bits[u]);
+            } else {
+                put_vec<I, OF, false>(out, x[u], 0);
             }
         }
     }
     // the elements before and behind the vectors (all of them where the tensors are not
-    // 16-byte aligned)
-    const int ends = A.vec ? min(len, 2 * VE) : len;
-    for (int i = 0; i < rows; ++i) {
-        const int m = mask_of[i];
-        const long long n0 = (row0 + i) * A.V + v0;
-        const int head = A.vec ? min(len, static_cast<int>(-n0 & (VE - 1))) : len;
+    // 16-byte aligned), with their adjustment
+    const int ends = A.vec ? 2 * VE : len;
+    for (int e = t; e < rows * ends; e += NTJ) {
+        const int i = e / ends, m = mask_of[i];
+        const int head = A.vec ? min(len, static_cast<int>(-row_at(i) & (VE - 1))) : len;
         const int tail = (len - head) / VE * VE + head;    // the first behind the vectors
-        if (!stored(m)) continue;
-        for (int e = t; e < ends; e += NTJ) {
-            const int v = e < head ? e : tail + (e - head);
-            if (v >= len) break;
-            const bool ok = m < 0 || (admit[static_cast<long long>(m) * (4ll * A.W) + ((v0 + v) >> 3)] >> ((v0 + v) & 7) & 1);
-            put_one<I, OF>(A.out, n0 + v, m == BROKEN ? NAN : ok ? I::one(A.in, n0 + v) : -INFINITY);
-        }
+        const int v = e % ends < head ? e % ends : tail + (e % ends - head);
+        if (v >= len || (A.inplace && m == OPEN && !dense)) continue;
+        const bool ok = m < 0 || (mask_row(m)[(v0 + v) >> 3] >> ((v0 + v) & 7) & 1);
+        float y = m == BROKEN ? NAN : ok ? I::one(A.in, row_at(i) + v) : -INFINITY;
+        if (dense && ok && m != BROKEN && cnt[v] != 0) y = adjusted(y, v, i);
+        put_one<I, OF>(A.out, row_at(i) + v, y);
     }
-    if (active == 0) return;
+    if (todo == 0) return;
     __builtin_amdgcn_s_waitcnt(0);                         // the stores above land before those below
     __syncthreads();
-    // the listed tokens: item e is entry e % active in row e / active
-    const unsigned long long bo = static_cast<unsigned long long>(b) * A.nb;
-    const int items = rows * active;
-    const float inv = 1.0f / static_cast<float>(active);
-    for (int e0 = t; e0 < items; e0 += U * NTJ) {
-        float x[U];
-        int v[U], row[U];
+    for (int e0 = t; e0 < todo; e0 += U * NTJ) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            int i, v;
             const int e = e0 + u * NTJ;
-            row[u] = -1;
-            x[u] = 0.0f;
-            if (e >= items) continue;
-            const int i = static_cast<int>((static_cast<float>(e) + 0.5f) * inv);  // exact: e < 2^19
-            v[u] = list[e - i * active];
-            const int m = mask_of[i];
-            if (m == OPEN || (m >= 0 && (admit[static_cast<long long>(m) * (4ll * A.W) + ((v0 + v[u]) >> 3)] >>
-                                         ((v0 + v[u]) & 7) & 1))) {
-                row[u] = i;
-                x[u] = I::one(A.in, (row0 + i) * A.V + v0 + v[u]);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (row[u] < 0) continue;
-            const unsigned c = cnt[v[u]], o = BIAS ? own[v[u]] : NOBIAS;
-            unsigned num = c & (DRAFT - 1);
-            if ((c & DRAFT) != 0)
-                for (int j = 0; j < row[u]; ++j) num += drafts[j] == v[u];
-            float y = x[u];
-            if ((c & SEEN) != 0 || num > 0) y = y > 0.0f ? y / rep : y * rep;
-            if (num > 0) y = y - freq * static_cast<float>(num) - pres;
-            if (o != NOBIAS) {
-                float bias = A.bias_val[bo + o];
-                if (dup)
-                    for (int j = static_cast<int>(o) + 1; j < A.nb; ++j)
-                        if (A.bias_tok[bo + j] == v0 + v[u]) bias += A.bias_val[bo + j];
-                y += bias;
-            }
-            put_one<I, OF>(A.out, (row0 + row[u]) * A.V + v0 + v[u], y);
+            if (e >= todo || !entry(e, i, v)) continue;
+            const long long n = (row0 + i) * A.V + v0 + v;
+            put_one<I, OF>(A.out, n, adjusted(e0 == t ? early[u] : I::one(A.in, n), v, i));
         }
     }
 }
@@ -1636,8 +1714,8 @@ int spec_adjust(const void* logits, int32_t B, int32_t R, int32_t V, int dtype, 
                     "(got B=%d k=%d R=%d V=%d)", SPEC_MAX_K, B, k, R, V);
     if (static_cast<unsigned long long>(B) * R * static_cast<unsigned long long>(V) > (1ull << 46))
         return fail(SPEC_ERR_SHAPE, "B*R*V is too large");
-    if (H < 0 || H > (1 << 30) - 1 || n_bias < 0 || n_bias > 65536 || n_admit < 0)
-        return fail(SPEC_ERR_SHAPE, "need 0 <= H < 2^30, 0 <= n_bias <= 65536, n_admit >= 0 (got %d, %d, %d)", H,
+    if (H < 0 || H > (1 << 29) - 1 || n_bias < 0 || n_bias > 65536 || n_admit < 0)
+        return fail(SPEC_ERR_SHAPE, "need 0 <= H < 2^29, 0 <= n_bias <= 65536, n_admit >= 0 (got %d, %d, %d)", H,
                     n_bias, n_admit);
     if (!logits || !out) return fail(SPEC_ERR_NULL, "logits or out is NULL");
     if (k > 0 && !draft_tokens) return fail(SPEC_ERR_NULL, "draft_tokens is NULL");
@@ -1676,7 +1754,7 @@ int spec_adjust(const void* logits, int32_t B, int32_t R, int32_t V, int dtype, 
     const long long rounds = (B * least + ADJ_SLOTS - 1) / ADJ_SLOTS;
     long long nseg = rounds * ADJ_SLOTS / B;
     const long long line = static_cast<long long>(R) * V * static_cast<long long>(es + eo);
-    if (H > 0 && nseg > line / (4ll * H)) nseg = line / (4ll * H);
+    if (H > 0 && nseg > line / (2ll * H)) nseg = line / (2ll * H);
     if (nseg > (V + SEG_MIN - 1) / SEG_MIN) nseg = (V + SEG_MIN - 1) / SEG_MIN;
     if (nseg < least) nseg = least;
     A.seg = static_cast<int>(((V + nseg - 1) / nseg + 63) / 64 * 64);
