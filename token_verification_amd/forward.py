@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -64,23 +65,31 @@ def _raise(rc: int):
     raise SpecVerifyError(rc, forward_lib().spec_forward_last_error().decode())
 
 
+# The small calls' time is the host's, so these go straight to what torch.cuda's functions of
+# similar names call.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+
+
 def _call(fn, dev: torch.device, *args) -> None:
     """fn(*args, stream) on dev's current stream, with dev the current device."""
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if index == _current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(index))
     if rc != 0:
         _raise(rc)
 
 
-_Stride = ctypes.c_int64 * 3
+_pack_stride = struct.Struct("3q").pack
 
 
-def _stride(t: torch.Tensor):
+def _stride(t: torch.Tensor) -> bytes:
     s = t.stride()
-    return _Stride(s[0], s[1], s[2])
+    return _pack_stride(s[0], s[1], s[2])
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -88,15 +97,17 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _check(t, name: str, shape, dtype, dev: torch.device) -> None:
-    """A dense tensor of this shape and dtype (any of them if a tuple) on dev."""
-    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.device != dev \
-            or not t.is_contiguous():
+    """A dense tensor of this shape and dtype on dev."""
+    try:
+        fine = t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()
+    except AttributeError:
+        fine = False
+    if not fine:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {dev}")
 
 
-def _check_strided(t, name: str, dev: torch.device) -> None:
+def _check_strided(t, name: str, es: int, dev: torch.device) -> None:
     """A [.., .., .., D] tensor whose rows the library can load in 16-byte pieces."""
-    es = t.element_size()
     s = t.stride()
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
@@ -107,6 +118,8 @@ def _check_strided(t, name: str, dev: torch.device) -> None:
 
 def _overlaps_itself(t: torch.Tensor) -> bool:
     """Whether two indices of t may share a place (an expanded cache, say)."""
+    if t.is_contiguous():
+        return False
     extent = 1
     for stride, size in sorted(zip(t.stride(), t.shape)):
         if size > 1:
@@ -119,27 +132,33 @@ def _overlaps_itself(t: torch.Tensor) -> bool:
 def _check_cache(k_cache, v_cache, page_table, kv_len, draft_len, k_scale, v_scale, B: int, D: int, dtype,
                  dev: torch.device):
     """(Hkv, pages, page_size, max_pages, cache dtype code) of a paged cache."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.shape[3] != D:
-            raise ValueError(f"{name} must be a [pages, Hkv, page_size, D] tensor with D = {D}")
-        if t.dtype != dtype and t.dtype != torch.float8_e4m3fn:
-            raise ValueError(f"{name} must be {dtype} or float8_e4m3fn (got {t.dtype})")
-        _check_strided(t, name, dev)
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
-        raise ValueError("k_cache and v_cache must have one shape and dtype")
-    pages, Hkv, page_size, _ = k_cache.shape
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] != B:
+    try:
+        shape, kind, es = k_cache.shape, k_cache.dtype, k_cache.element_size()
+        fine = len(shape) == 4 and shape[3] == D and v_cache.shape == shape and v_cache.dtype is kind
+    except AttributeError:
+        fine = False
+    if not fine:
+        raise ValueError(f"k_cache and v_cache must be [pages, Hkv, page_size, D] tensors of one shape and dtype, "
+                         f"with D = {D}")
+    e4m3 = kind is torch.float8_e4m3fn
+    if not e4m3 and kind is not dtype:
+        raise ValueError(f"k_cache and v_cache must be {dtype} or float8_e4m3fn (got {kind})")
+    _check_strided(k_cache, "k_cache", es, dev)
+    _check_strided(v_cache, "v_cache", es, dev)
+    pages, Hkv, page_size, _ = shape
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 [B, max_pages] tensor")
-    _check(page_table, "page_table", page_table.shape, torch.int32, dev)
+    max_pages = page_table.shape[1]
+    _check(page_table, "page_table", (B, max_pages), torch.int32, dev)
     _check(kv_len, "kv_len", (B,), torch.int32, dev)
     if draft_len is not None:
         _check(draft_len, "draft_len", (B,), torch.int32, dev)
-    if k_cache.dtype == torch.float8_e4m3fn:
+    if e4m3:
         _check(k_scale, "k_scale (of a float8_e4m3fn cache)", (Hkv,), torch.float32, dev)
         _check(v_scale, "v_scale (of a float8_e4m3fn cache)", (Hkv,), torch.float32, dev)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale go with a float8_e4m3fn cache only")
-    return Hkv, pages, page_size, page_table.shape[1], _CACHE[k_cache.dtype]
+    return Hkv, pages, page_size, max_pages, _CACHE[kind]
 
 
 def spec_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -159,19 +178,19 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     """
     if not isinstance(k, torch.Tensor) or k.dim() != 4 or not k.is_cuda or k.dtype not in _QKV:
         raise ValueError("k must be a bfloat16 or float16 [B, R, Hkv, D] device tensor")
-    if not isinstance(v, torch.Tensor) or v.shape != k.shape or v.dtype != k.dtype:
+    shape, dtype, dev = k.shape, k.dtype, k.device
+    if not isinstance(v, torch.Tensor) or v.shape != shape or v.dtype is not dtype:
         raise ValueError("v must match k's shape and dtype")
-    B, R, H, D = k.shape
-    dev = k.device
-    _check_strided(k, "k", dev)
-    _check_strided(v, "v", dev)
+    B, R, H, D = shape
+    _check_strided(k, "k", 2, dev)
+    _check_strided(v, "v", 2, dev)
     Hkv, pages, page_size, max_pages, code = _check_cache(k_cache, v_cache, page_table, kv_len, draft_len, k_scale,
-                                                          v_scale, B, D, k.dtype, dev)
+                                                          v_scale, B, D, dtype, dev)
     if H != Hkv:
         raise ValueError(f"k holds {H} heads, the cache {Hkv}")
     if _overlaps_itself(k_cache) or _overlaps_itself(v_cache):
         raise ValueError("k_cache and v_cache must hold every element at a place of its own")
-    _call(forward_lib().spec_kv_append, dev, k.data_ptr(), _stride(k), v.data_ptr(), _stride(v), _QKV[k.dtype],
+    _call(forward_lib().spec_kv_append, dev, k.data_ptr(), _stride(k), v.data_ptr(), _stride(v), _QKV[dtype],
           B, R, H, D, k_cache.data_ptr(), _stride(k_cache), v_cache.data_ptr(), _stride(v_cache), code, pages,
           page_size, page_table.data_ptr(), max_pages, kv_len.data_ptr(), _ptr(draft_len), _ptr(k_scale),
           _ptr(v_scale))
@@ -185,9 +204,9 @@ def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
     """One workspace per (device, stream). A call that is captured into a graph gets
     one of its own, from the graph's memory: graphs captured on one stream may be
     replayed on different ones at the same time."""
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    key = (dev.index, _raw_stream(dev.index))
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -215,17 +234,17 @@ def spec_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     """
     if not isinstance(q, torch.Tensor) or q.dim() != 4 or not q.is_cuda or q.dtype not in _QKV:
         raise ValueError("q must be a bfloat16 or float16 [B, R, Hq, D] device tensor")
-    B, R, Hq, D = q.shape
-    dev = q.device
-    _check_strided(q, "q", dev)
+    shape, dtype, dev = q.shape, q.dtype, q.device
+    B, R, Hq, D = shape
+    _check_strided(q, "q", 2, dev)
     Hkv, pages, page_size, max_pages, code = _check_cache(k_cache, v_cache, page_table, kv_len, draft_len, k_scale,
-                                                          v_scale, B, D, q.dtype, dev)
+                                                          v_scale, B, D, dtype, dev)
     if slopes is not None:
         _check(slopes, "slopes", (Hq,), torch.float32, dev)
     if out is None:
-        out = torch.empty((B, R, Hq, D), dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=dtype, device=dev)
     else:
-        _check(out, "out", (B, R, Hq, D), q.dtype, dev)
+        _check(out, "out", shape, dtype, dev)
         if out.data_ptr() % 16:
             raise ValueError("out must be 16-byte aligned")
     key = (B, R, Hq, Hkv, D, code, page_size, max_pages)
@@ -237,11 +256,11 @@ def spec_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                                       f"page_size={page_size} max_pages={max_pages}")
         _need_cache[key] = need
     ws = _workspace(dev, need) if workspace is None else _user_workspace(workspace, dev, need)
-    _call(forward_lib().spec_attention, dev, q.data_ptr(), _stride(q), _QKV[q.dtype], B, R, Hq, Hkv, D,
+    _call(forward_lib().spec_attention, dev, q.data_ptr(), _stride(q), _QKV[dtype], B, R, Hq, Hkv, D,
           k_cache.data_ptr(), _stride(k_cache), v_cache.data_ptr(), _stride(v_cache), code, pages, page_size,
           page_table.data_ptr(), max_pages, kv_len.data_ptr(), _ptr(draft_len),
           1.0 / math.sqrt(D) if scale is None else float(scale), float(softcap), int(window), _ptr(slopes),
-          _ptr(k_scale), _ptr(v_scale), out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+          _ptr(k_scale), _ptr(v_scale), out.data_ptr(), ws.data_ptr(), ws.nbytes)
     return out
 
 
@@ -273,8 +292,8 @@ def spec_adjust(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *,
         raise ValueError("logits must be a float32 or bfloat16 [B, R, V] device tensor")
     if not logits.is_contiguous():
         raise ValueError("logits must be contiguous")
-    B, R, V = logits.shape
-    dev = logits.device
+    shape, kind, dev = logits.shape, logits.dtype, logits.device
+    B, R, V = shape
     k = 0
     if tokens is not None:
         if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2:
@@ -323,10 +342,10 @@ def spec_adjust(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *,
     if draft_len is not None:
         _check(draft_len, "draft_len", (B,), torch.int32, dev)
     if out is None:
-        dtype = logits.dtype if out_dtype is None else out_dtype
-        if dtype != logits.dtype and dtype != torch.float32:
+        dtype = kind if out_dtype is None else out_dtype
+        if dtype != kind and dtype != torch.float32:
             raise ValueError(f"out_dtype must be float32 or the logits' dtype (got {dtype})")
-        out = torch.empty((B, R, V), dtype=dtype, device=dev)
+        out = torch.empty(shape, dtype=dtype, device=dev)
     else:
         _check(out, "out", (B, R, V), getattr(out, "dtype", None) if out_dtype is None else out_dtype, dev)
         if out.dtype != logits.dtype and out.dtype != torch.float32:
