@@ -96,7 +96,7 @@ int spec_kv_append(const void* k, const int64_t* k_stride, const void* v, const 
  * initialisation needed, one call at a time. 1 <= R <= SPEC_MAX_K + 1,
  * 1 <= Hkv <= 1024, Hq a multiple of Hkv up to 1024, otherwise the limits of
  * spec_kv_append. Errors: as there, plus SPEC_ERR_VALUE (scale not finite, softcap
- * negative or not finite, window negative) and SPEC_ERR_WORKSPACE.
+ * negative, not finite or below 1e-30 |scale| without being 0, window negative) and SPEC_ERR_WORKSPACE.
  */
 int spec_attention(const void* q, const int64_t* q_stride, int dtype, int32_t B, int32_t R, int32_t Hq, int32_t Hkv,
                    int32_t D, const void* k_cache, const int64_t* k_cache_stride, const void* v_cache,

@@ -67,7 +67,10 @@ ATTENTIONS = [
     dict(R=2, slopes=True, lens=[90, 17]), dict(R=3, softcap=30.0, window=20, slopes=True, lens=[300, 10]),
     dict(R=5, draft_len=[0, 4], lens=[40, 12]), dict(B=3, R=5, draft_len=[-1, 2, 5], lens=[40, 12, 7]),
     dict(R=9, G=8, Hkv=1, lens=[100, 3]), dict(page=1, lens=[40, 9]), dict(page=1024, lens=[700, 5]),
-    dict(B=5, R=2, lens=[0, 500, 3, 129, 64]), dict(scale=0.0), dict(scale=-0.3), dict(strided=False),
+    dict(B=5, R=2, lens=[0, 500, 3, 129, 64]), dict(B=70, lens=[(11 * b) % 150 for b in range(70)], G=1, Hkv=1),
+    dict(R=7, G=5, Hkv=1, lens=[200, 33], D=128), dict(R=6, G=8, Hkv=1, cache="e4m3", lens=[100, 64], D=128),
+    dict(R=8, G=8, Hkv=1, cache="e4m3", lens=[70, 0]), dict(R=5, G=7, Hkv=1, window=20, lens=[90, 5], page=8),
+    dict(R=9, G=4, Hkv=1, D=256, lens=[40, 65]), dict(R=25, G=8, Hkv=1, lens=[30, 2]), dict(scale=0.0), dict(scale=-0.3), dict(strided=False),
 ]
 
 
@@ -115,7 +118,8 @@ def poison(a, R, what, cache=None):
     return dict(a, k_cache=k, v_cache=v)
 
 
-@pytest.mark.parametrize("kw", [dict(), dict(window=21), dict(cache="e4m3"), dict(draft_len=[1, 0, 3])], ids=str)
+@pytest.mark.parametrize("kw", [dict(), dict(window=21), dict(cache="e4m3"), dict(draft_len=[1, 0, 3]), dict(G=10),
+                                dict(G=10, window=21), dict(G=20, cache="e4m3", draft_len=[3, 2, 0])], ids=str)
 @pytest.mark.parametrize("what", [float("nan"), float("inf")])
 def test_attention_ignores_places_nobody_sees(run, kw, what):
     a = fc.make_attention(6, B=3, R=4, lens=[77, 0, 30], **kw)
@@ -125,16 +129,27 @@ def test_attention_ignores_places_nobody_sees(run, kw, what):
 @pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("which", ["k_cache", "v_cache"])
 @pytest.mark.parametrize("window", [0, 3])
-def test_attention_bad_value_reaches_only_who_sees_it(run, what, which, window):
+@pytest.mark.parametrize("G", [2, 9])
+def test_attention_bad_value_reaches_only_who_sees_it(run, what, which, window, G):
     """A non-finite key or value of the last draft: the earlier tokens do not see it; one
     just before the first token's window end: the later ones do not."""
-    a = fc.make_attention(7, B=2, R=4, lens=[45, 2], window=window)
+    a = fc.make_attention(7, B=2, R=4, lens=[45, 2], window=window, G=G)
     for t, b in ((48, 0), (5, 1), (44, 0)):
         x = a[which].clone()
         ps = x.shape[2]
         x[a["page_table"][b, t // ps], :, t % ps, 5] = what
         a2 = dict(a, **{which: x})
         fc.check_attention(run, a2, f"position {t}")
+
+
+def test_attention_shared_pages(run):
+    """Two sequences that share their first pages (a common prefix), and one page twice in a
+    sequence."""
+    a = fc.make_attention(16, B=3, R=2, lens=[100, 90, 70])
+    table = a["page_table"].clone()
+    table[1, :4] = table[0, :4]
+    table[2, 2] = table[2, 0]
+    fc.check_attention(run, dict(a, page_table=table))
 
 
 def test_attention_extreme_scores(run):

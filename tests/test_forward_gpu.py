@@ -56,7 +56,10 @@ def test_append_e4m3_rounds_every_value(run, dtype):
     dict(B=2, R=65, Hkv=1, G=2, lens=[100, 0]), dict(B=1, R=17, Hkv=1, G=16, D=128, lens=[513]),
     dict(B=2, R=4, Hkv=3, G=7, D=128, cache="e4m3", lens=[2048, 2047]), dict(B=300, lens=[(7 * b) % 40 for b in range(300)]),
     dict(B=2, R=3, Hkv=2, D=128, window=500, softcap=50.0, lens=[3001, 499], dtype="f16"),
-    dict(B=1, Hkv=20, G=1, lens=[1500], slopes=True), dict(B=1, R=2, D=256, cache="e4m3", dtype="f16", lens=[1200], page=128),
+    dict(B=1, Hkv=20, G=1, lens=[1500], slopes=True), dict(B=100, R=2, lens=[(97 * b) % 700 for b in range(100)]),
+    dict(B=600, Hkv=1, G=2, lens=[(131 * b) % 900 for b in range(600)]), dict(B=2, R=9, G=8, Hkv=2, D=128, lens=[2500, 60]),
+    dict(B=2, R=6, G=7, Hkv=2, D=128, cache="e4m3", lens=[3000, 100]), dict(B=1, R=8, G=8, Hkv=1, D=256, lens=[1000]),
+    dict(B=2, R=65, G=8, Hkv=1, D=128, lens=[700, 0]), dict(B=1, R=12, G=16, Hkv=1, D=128, lens=[3000], window=1000), dict(B=1, R=2, D=256, cache="e4m3", dtype="f16", lens=[1200], page=128),
 ], ids=str)
 def test_attention(run, kw):
     fc.check_attention(run, fc.make_attention(3, **kw))
@@ -79,7 +82,8 @@ def test_attention_window_over_unmapped_pages(run, page):
     fc.check_attention(run, cpu.unmap(a, page, 33))
 
 
-@pytest.mark.parametrize("kw", [dict(), dict(window=21), dict(cache="e4m3"), dict(draft_len=[1, 0, 3])], ids=str)
+@pytest.mark.parametrize("kw", [dict(), dict(window=21), dict(cache="e4m3"), dict(draft_len=[1, 0, 3]), dict(G=10),
+                                dict(G=10, window=21), dict(G=20, cache="e4m3", draft_len=[3, 2, 0])], ids=str)
 @pytest.mark.parametrize("what", [float("nan"), float("inf")])
 def test_attention_ignores_places_nobody_sees(run, kw, what):
     a = fc.make_attention(6, B=3, R=4, lens=[777, 0, 30], **kw)
@@ -89,8 +93,13 @@ def test_attention_ignores_places_nobody_sees(run, kw, what):
 @pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("which", ["k_cache", "v_cache"])
 @pytest.mark.parametrize("window", [0, 3])
-def test_attention_bad_value_reaches_only_who_sees_it(run, what, which, window):
-    cpu.test_attention_bad_value_reaches_only_who_sees_it(run, what, which, window)
+@pytest.mark.parametrize("G", [2, 9])
+def test_attention_bad_value_reaches_only_who_sees_it(run, what, which, window, G):
+    cpu.test_attention_bad_value_reaches_only_who_sees_it(run, what, which, window, G)
+
+
+def test_attention_shared_pages(run):
+    cpu.test_attention_shared_pages(run)
 
 
 def test_attention_extreme_scores(run):

@@ -78,9 +78,9 @@ struct Cache {
 // if its length is out of range (a row in use has at least one).
 __device__ inline int seq_rows(const Cache& C, int b, int& kv) {
     kv = C.kv_len[b];
-    const int n = C.draft_len ? C.draft_len[b] + 1 : C.R;
+    // (a draft_len of INT_MAX wraps to a negative n: also out of range)
+    const int n = C.draft_len ? static_cast<int>(static_cast<unsigned>(C.draft_len[b]) + 1u) : C.R;
     const long long cap = static_cast<long long>(C.max_pages) << C.shift;
-    // a draft_len of INT_MAX wraps to a negative n: also out of range
     return kv < 0 || n < 1 || n > C.R || static_cast<long long>(kv) + n > cap ? 0 : n;
 }
 
@@ -1671,9 +1671,10 @@ int spec_attention(const void* q, const int64_t* q_stride, int dtype, int32_t B,
     if (rc != SPEC_OK) return rc;
     if (Hq < Hkv || Hq > 1024 || Hq % Hkv != 0)
         return fail(SPEC_ERR_SHAPE, "Hq must be a multiple of Hkv up to 1024 (got Hq=%d Hkv=%d)", Hq, Hkv);
-    if (!(fabsf(scale) <= F32_MAX) || !(softcap >= 0.0f && softcap <= F32_MAX) || window < 0)
-        return fail(SPEC_ERR_VALUE, "scale must be finite, softcap finite and >= 0, window >= 0 (got %g, %g, %d)",
-                    static_cast<double>(scale), static_cast<double>(softcap), window);
+    if (!(fabsf(scale) <= F32_MAX) || !(softcap >= 0.0f && softcap <= F32_MAX) || window < 0 ||
+        (softcap > 0.0f && !(fabsf(scale) / softcap <= 1e30f)))
+        return fail(SPEC_ERR_VALUE, "scale must be finite, softcap finite and >= 0 (0, or at least 1e-30 |scale|), "
+                    "window >= 0 (got %g, %g, %d)", static_cast<double>(scale), static_cast<double>(softcap), window);
     if (!q || !q_stride || !out) return fail(SPEC_ERR_NULL, "q, its strides or out is NULL");
     if (!aligned(q, 16) || !strides_ok(q_stride, 2, A.qs) || !aligned(out, 16))
         return fail(SPEC_ERR_ALIGN, "q and out must be 16-byte aligned and q's strides multiples of 8 elements");
