@@ -501,11 +501,11 @@ struct AttnShape : TileShape<D, E4M3> {
     static constexpr int PARTS = ROWS ? 1 : NWQ;           // partial results per query row
     // Workgroups per CU (waves per SIMD): as many as LDS and the registers allow: the
     // accumulators, the queries, scores and weights, one tile's operands and about 70
-    // more (REST; with 90 at D = 64, where 128 registers spill a few: R * G = 1, 32 x 2047
+    // more (REST; with 95 at D = 64, where 128 registers spill a few: R * G = 1, 32 x 2047
     // keys, 83 us at four waves to a SIMD, 73 at three). Then as many tiles in LDS as fit: the more loads in flight, the nearer to
     // HBM's rate. With ROWS one tile is not in flight but in use.
     static constexpr int LDS_CU = 160 * 1024, MORE = 4 * 1024;             // per CU; beside the tiles
-    static constexpr int REST = D == 64 && !E4M3 ? 90 : D == 128 && !ROWS && MT == 3 ? 50 : 70;
+    static constexpr int REST = D == 64 && (!E4M3 || ROWS) ? 95 : D == 128 && !ROWS && MT == 3 ? 50 : 70;
     static constexpr int REGS = 512 / (D * MT / 4 + D * MT / 8 + 12 * MT + D / (E4M3 ? 8 : 4) + REST);
     static constexpr int fit(int occ) { return (LDS_CU / occ - MORE) / STAGE; }
     static constexpr int occupancy() {
