@@ -25,11 +25,11 @@
  *
  * Paged cache: page_table [B, max_pages] int32; position t of batch row b is token
  * t % page_size of page page_table[b, t / page_size]. page_size is a power of two up to
- * 65536. k_cache and v_cache hold `pages` pages; element (page, h, token, j) of cache
+ * 65536, and max_pages * page_size at most 2^30. k_cache and v_cache hold `pages` pages; element (page, h, token, j) of cache
  * head h is at page * stride[0] + h * stride[1] + token * stride[2] + j (strides in
  * elements, j < D contiguous), so both the [pages, Hkv, page_size, D] and the
  * [pages, page_size, Hkv, D] order are served. Base pointers are 16-byte aligned and
- * strides multiples of 16 bytes. Offsets are 64-bit. The cache holds bfloat16 or float16
+ * strides multiples of 16 bytes, tokens at most 2^27 bytes apart. Offsets are 64-bit. The cache holds bfloat16 or float16
  * (the type of the new keys, values and queries), or e4m3 (OCP, finite range +-448) with
  * one positive float32 scale per cache head: value = code * scale[h].
  */
@@ -88,8 +88,9 @@ int spec_kv_append(const void* k, const int64_t* k_stride, const void* v, const 
  * Only cache places that a used token sees are used: pages before every window and behind
  * the last token may be unmapped, and NaN or infinities there change nothing.
  * Products of q and k are summed in float32, the softmax and the sums are float32; the
- * weights exp(s - m) are rounded once to q's dtype for the product with v. (m is a
- * running maximum up to 2^8 below the true one, so their magnitude is at most 2^8.)
+ * weights exp(s - m) are rounded once to q's dtype for the product with v. (m is at
+ * or below the true maximum, so their magnitude is at most 2^8, or 2^15 in float16, where
+ * the maximum's is at least 2^7.)
  * The length is split over workgroups, whose partial results are joined by a second
  * kernel; how it is split depends on the lengths on the device, not on the host.
  * Workspace: at least spec_attention_workspace_size() bytes, 256-byte aligned, no

@@ -16,6 +16,8 @@ import numpy as np
 U32 = 2.0 ** -24                                           # half a step, relative to the value
 HALF_STEP = {"f32": U32, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
 TINY = {"f32": 2.0 ** -126, "f16": 2.0 ** -24, "bf16": 2.0 ** -126}
+# the absolute half step of a weight below the smallest normal, where the largest weight is 1
+WEIGHT = {"f16": 2.0 ** -25 / 2.0 ** 7, "bf16": 2.0 ** -126}
 
 
 def e4m3_value(codes: np.ndarray) -> np.ndarray:
@@ -69,11 +71,15 @@ def attention_ref(q, k_cache, v_cache, table, kv_len, *, dtype, draft_len=None, 
     """(out, tolerance), both [B, R, Hq, D].
 
     Tolerance, with u half a step of dtype: the weights exp(s - m) are rounded to
-    dtype (u each; below dtype's smallest normal an absolute half step, at most TINY,
-    where the largest weight of the sum is at least 1), the scores
+    dtype (u each; below dtype's smallest normal an absolute half step, WEIGHT of the
+    largest weight), the scores
     carry the rounding of a D-term float32 product sum ((D + 4) U32 of sum |q k|
     scale), of the factors and the bias (8 U32 of the largest term; a tanh's absolute
-    2^-21 of the cap) and of exp2 (2^-21 with its argument's reduction), the sums over
+    2^-21 of the cap, or, for caps of 256 and more, where that is less, 2^-19 of the score:
+    the series' next term is 2^-21.5 of it below a quarter of the cap; above it, with
+    A = 2^-23, the argument's rounding moves 1 - 2 / (1 + e) by at most 0.45 A, exp2 by
+    0.5 A, the sum by 0.38 A, the reciprocal by 0.76 A and the difference by 0.5 A, together
+    2.6 A of at least tanh(1/4) = 0.245) and of exp2 (2^-21 with its argument's reduction), the sums over
     n tokens n U32 of their absolute value, and the result u of itself. A relative
     error d_t of weight t moves the result by p_t d_t (v_t - out).
     """
@@ -111,7 +117,7 @@ def attention_ref(q, k_cache, v_cache, table, kv_len, *, dtype, draft_len=None, 
                         ds = (D + 4) * U32 * raw + 8 * U32 * np.abs(s)
                         if softcap:
                             s = softcap * np.tanh(s / softcap)
-                            ds = ds + 2.0 ** -21 * softcap
+                            ds = ds + np.minimum(2.0 ** -21 * softcap, 2.0 ** -19 * np.abs(s) if softcap >= 256 else np.inf)
                         if slopes is not None:
                             away = slopes[h * G + g] * (np.arange(first, kv + i + 1) - (kv + i))
                             s = s + away
@@ -120,7 +126,7 @@ def attention_ref(q, k_cache, v_cache, table, kv_len, *, dtype, draft_len=None, 
                         o = (p @ Vv) / p.sum()
                         d = u + ds + 2.0 ** -21 + len(s) * U32
                         t = ((p * d) @ np.abs(Vv) + (p * d).sum() * np.abs(o)) / p.sum()
-                        t = t + TINY[dtype] * np.abs(Vv).sum(0) / p.sum()
+                        t = t + WEIGHT[dtype] * np.abs(Vv).sum(0) / p.sum()
                         out[b, i, h * G + g] = o
                         tol[b, i, h * G + g] = 1.01 * t + u * (np.abs(o) + 1.01 * t) + TINY[dtype]
     return out, tol

@@ -79,6 +79,34 @@ def test_attention(run, kw):
     fc.check_attention(run, fc.make_attention(3, **kw))
 
 
+@pytest.mark.parametrize("softcap", [255.0, 256.0, 5000.0, 1e8, 1e30, 3e38])
+def test_attention_large_softcap(run, softcap):
+    """A cap far above the scores leaves them as they are."""
+    fc.check_attention(run, fc.make_attention(15, R=2, softcap=softcap, sharp=10.0, lens=[90, 17]))
+
+
+def test_attention_softcap_between_series_and_exponential(run):
+    """Scores on both sides of a quarter of the cap."""
+    a = fc.make_attention(16, R=2, G=4, softcap=300.0, sharp=1.0, lens=[120, 40])
+    fc.check_attention(run, dict(a, q=a["q"] * torch.tensor([4.0, 20.0, 60.0, 300.0] * 2)[:, None].to(a["q"].dtype)))
+
+
+@pytest.mark.parametrize("cache", ["same", "e4m3"])
+def test_attention_float16_sums_of_small_weights(run, cache):
+    """Many weights of about 2^-24 of the largest, whose value is zero."""
+    a = fc.make_attention(17, B=1, Hkv=1, dtype="f16", cache=cache, lens=[1500])
+    ones = torch.ones_like(a["k_cache"].float())
+    first = int(a["page_table"][0, 0])
+    k, v = ones * 0.0, ones * 200.0
+    k[..., 0] = -16.0
+    k[first, :, 0], v[first, :, 0] = 0.0, 0.0
+    q = torch.zeros_like(a["q"])
+    q[..., 0] = torch.tensor([1.0, 1.0166])
+    if cache == "e4m3":
+        a.update(k_scale=torch.ones(1), v_scale=torch.ones(1))
+    fc.check_attention(run, dict(a, q=q, k_cache=k.to(a["k_cache"].dtype), v_cache=v.to(a["v_cache"].dtype), scale=1.0))
+
+
 def test_attention_bad_rows(run):
     a = fc.make_attention(4, B=7, R=2, lens=[30, 9, 8, 4, 20, 40, 12])
     fc.check_attention(run, bad_rows(a, 16))

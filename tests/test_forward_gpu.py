@@ -65,6 +65,20 @@ def test_attention(run, kw):
     fc.check_attention(run, fc.make_attention(3, **kw))
 
 
+@pytest.mark.parametrize("softcap", [255.0, 256.0, 5000.0, 1e8, 1e30, 3e38])
+def test_attention_large_softcap(run, softcap):
+    cpu.test_attention_large_softcap(run, softcap)
+
+
+def test_attention_softcap_between_series_and_exponential(run):
+    cpu.test_attention_softcap_between_series_and_exponential(run)
+
+
+@pytest.mark.parametrize("cache", ["same", "e4m3"])
+def test_attention_float16_sums_of_small_weights(run, cache):
+    cpu.test_attention_float16_sums_of_small_weights(run, cache)
+
+
 def test_attention_bad_rows(run):
     fc.check_attention(run, cpu.bad_rows(fc.make_attention(4, B=7, R=2, lens=[30, 9, 8, 4, 20, 40, 12]), 16))
 

@@ -34,6 +34,8 @@ struct Bf16 {
     using type = __bf16;
     static constexpr bool IS_BF16 = true;
     static constexpr unsigned EXP = 0x7f80u;               // exponent bits: all set = not finite
+    // log2 of the weight of a running maximum when it is set, and of the largest weight
+    static constexpr float TOP = 0.0f, LAZY = 8.0f;
     __device__ static inline float lo(unsigned w) { return bits_f32(w << 16); }
     __device__ static inline float hi(unsigned w) { return bits_f32(w & 0xffff0000u); }
 };
@@ -42,6 +44,9 @@ struct F16 {
     using type = _Float16;
     static constexpr bool IS_BF16 = false;
     static constexpr unsigned EXP = 0x7c00u;
+    // (near the top of the type's range, so that small weights keep their bits: the smallest
+    // normal one is 2^-21 of the maximum's)
+    static constexpr float TOP = 7.0f, LAZY = 15.0f;
     __device__ static inline float lo(unsigned w) {
         return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<unsigned short>(w)));
     }
@@ -169,9 +174,9 @@ __global__ __launch_bounds__(NTA) void append_kernel(AppendParams A) {
 // {4g..4g+3, 16+4g..16+4g+3} for lane group g; the A operand, columns of V in that
 // order, comes from LDS by transposing reads (ds_read_b64_tr_b16, or _tr_b8 for e4m3).
 // No score or weight ever crosses lanes. The running maximum of a row moves only when
-// a score exceeds it by more than 2^8 in weight (checked by a vote), so the two
+// a score exceeds it by 2^8 in weight (checked by a vote), so the two
 // exchanges and the rescaling that go with a new maximum are rare; weights are then
-// at most 2^8, and sums and accumulators are float32.
+// at most 2^8 (float16: 2^15, from 2^7 on), and sums and accumulators are float32.
 //
 // Each of a workgroup's four waves walks its own tiles of 32 keys with its own
 // accumulators, through its own part of LDS, and never waits for another wave: keys
@@ -194,7 +199,7 @@ constexpr int TT = 32;                                     // keys of a wave's t
 constexpr int TU = TT * NWQ;                               // keys of a unit
 constexpr int CUS = 256;
 constexpr int NT_LOAD = 2;                                 // cache policy: non-temporal (read once)
-constexpr float LAZY = 8.0f;                               // log2 of the largest weight
+constexpr float CAP_FINE = 256.0f;                         // softcaps from here on take the more exact tanh
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
@@ -758,7 +763,22 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
                 }
             }
             // scores in units of log2, masked
-            if (A.softcap > 0.0f) {                        // cap tanh(v / cap) = cap (1 - 2 / (1 + e^(2 v / cap)))
+            if (A.softcap >= CAP_FINE) {
+                // The form below is off by 2^-21 of the cap, which for a large one is more than
+                // the scores' own rounding. Here small y = v / cap take tanh's series (its
+                // next term is 2^-21 of it at y = 1/4).
+                const float by = scale / A.softcap, factor = scale * LOG2E;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float v = sc[j / 4][mt][j % 4], y = v * by, y2 = y * y;
+                        const float e = __builtin_amdgcn_exp2f(y * (2.0f * LOG2E));
+                        const float far = (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e)) * A.softcap * LOG2E;
+                        const float near = v * factor * (1.0f + y2 * (-1.0f / 3 + y2 * (2.0f / 15 - y2 * (17.0f / 315))));
+                        sc[j / 4][mt][j % 4] = fabsf(y) < 0.25f ? near : far;
+                    }
+            } else if (A.softcap > 0.0f) {                 // cap tanh(v / cap) = cap (1 - 2 / (1 + e^(2 v / cap)))
                 const float c = A.softcap * LOG2E, e2 = scale / A.softcap * 2.0f * LOG2E;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
@@ -801,7 +821,7 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
                 top[mt] = fmaxf(sc[0][mt][0], sc[0][mt][1]);
 #pragma unroll
                 for (int j = 2; j < 8; ++j) top[mt] = fmaxf(top[mt], sc[j / 4][mt][j % 4]);
-                up = up || top[mt] > mx[mt] + LAZY;
+                up = up || top[mt] > mx[mt] + T::LAZY;
             }
             if (__any(up)) {
 #pragma unroll
@@ -809,7 +829,7 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
                     float n = top[mt];
                     n = fmaxf(n, __shfl_xor(n, 16, 64));
                     n = fmaxf(n, __shfl_xor(n, 32, 64));
-                    n = fmaxf(n, mx[mt]);
+                    n = fmaxf(n - T::TOP, mx[mt]);
                     const float f = __builtin_amdgcn_exp2f(mx[mt] - n);
                     mx[mt] = n;
                     sum[mt] *= f;
