@@ -291,6 +291,20 @@ __device__ inline unsigned block_inclusive(Plan& P, unsigned v, unsigned& total)
     return before + x;
 }
 
+// x, hidden from the compiler: what is computed from it in a rare branch, or once per sequence,
+// is then computed there, not ahead of the loops and held in a register (or spilled) across
+// them. It saves the attention kernels 20 to 28 registers; an 8-bit cache with R * G = 40
+// spilled without it (201 MB of keys and values: 67 us, 58.5 with it).
+__device__ inline int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+__device__ inline long long fresh(long long x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // The batch's units, cut into `ranges` contiguous ranges whose sizes differ by at most one.
 struct Ranges {
     long long size, more;                                  // the first `more` ranges hold size + 1
@@ -298,8 +312,8 @@ struct Ranges {
 
     __device__ long long start(int w) const { return size * w + (w < more ? w : more); }
     __device__ int holding(long long u) const {
-        const long long c = more * (size + 1);
-        return static_cast<int>(u < c ? u / (size + 1) : more + (u - c) / size);
+        const long long n = fresh(size), c = more * (n + 1);
+        return static_cast<int>(u < c ? u / (n + 1) : more + (u - c) / n);
     }
 };
 
@@ -504,22 +518,33 @@ struct AttnShape : TileShape<D, E4M3> {
     static constexpr int STAGE = (ROWS ? 2 : 2 * NWQ) * HALF;              // of one tile (or one per wave)
     static constexpr int M16 = 16 * MT * (ROWS ? NWQ : 1); // query rows
     static constexpr int PARTS = ROWS ? 1 : NWQ;           // partial results per query row
-    // Workgroups per CU (waves per SIMD): as many as LDS and the registers allow: the
-    // accumulators, the queries, scores and weights, one tile's operands and about 70
-    // more (REST; with 95 at D = 64, where 128 registers spill a few: R * G = 1, 32 x 2047
-    // keys, 83 us at four waves to a SIMD, 73 at three). Then as many tiles in LDS as fit: the more loads in flight, the nearer to
-    // HBM's rate. With ROWS one tile is not in flight but in use.
+    // Row tiles whose queries stand in LDS, one copy for all waves, and are read for every tile
+    // of keys: where the registers of two waves per SIMD do not hold them (8-bit cache, R * G =
+    // 40, 201 MB of keys and values: 55.6 us, 58.5 with all of them in registers, which spills).
+    static constexpr int QL = D == 128 && MT == 3 && E4M3 && !ROWS ? 1 : 0;
+    // Workgroups per CU (waves per SIMD): at most what the registers allow, that is, the
+    // accumulators, the queries, scores and weights, one tile's operands and about 70 more.
+    // Of these, what has the most tiles in flight on the CU, for more loads in flight get
+    // nearer to HBM's rate (with ROWS one tile is not in flight but in use), and of these the
+    // most waves. 8-bit cache, D = 128, R * G = 8, 32 rows of 2048 keys: two workgroups of
+    // two tiles per wave 32.5 us, three of one 37.2; D = 64 in 16 bits, R * G = 24, 32 rows of
+    // 2048: two of two 34.2 us, three of one 39.0; R * G = 1, 32 rows of 1024: four of one
+    // 47.9 us, three of one 49.0.
     static constexpr int LDS_CU = 160 * 1024, MORE = 4 * 1024;             // per CU; beside the tiles
-    static constexpr int REST = D == 64 && (!E4M3 || ROWS) ? 95 : D == 128 && !ROWS && MT == 3 ? 50 : 70;
-    static constexpr int REGS = 512 / (D * MT / 4 + D * MT / 8 + 12 * MT + D / (E4M3 ? 8 : 4) + REST);
-    static constexpr int fit(int occ) { return (LDS_CU / occ - MORE) / STAGE; }
+    static constexpr int REGS = 512 / (D * MT / 4 + D * (MT - QL) / 8 + 12 * MT + D / (E4M3 ? 8 : 4) + 70);
+    static constexpr int tiles(int occ) {
+        const int n = (LDS_CU / occ - MORE) / STAGE, most = ROWS ? 6 : 4;
+        return n < most ? n : most;
+    }
     static constexpr int occupancy() {
-        int occ = REGS < 1 ? 1 : REGS > (ROWS ? 3 : 4) ? (ROWS ? 3 : 4) : REGS;
-        while (occ > 1 && fit(occ) < (ROWS ? 3 : 1)) --occ;
-        return occ;
+        const int most = REGS < 1 ? 1 : REGS > (ROWS ? 3 : 4) ? (ROWS ? 3 : 4) : REGS, idle = ROWS ? 1 : 0;
+        int best = 1;
+        for (int occ = 2; occ <= most; ++occ)
+            if (tiles(occ) > 2 * idle && occ * (tiles(occ) - idle) >= best * (tiles(best) - idle)) best = occ;
+        return best;
     }
     static constexpr int OCC = occupancy();
-    static constexpr int NS = fit(OCC) > (ROWS ? 6 : 4) ? (ROWS ? 6 : 4) : fit(OCC);
+    static constexpr int NS = tiles(OCC);
     static_assert(NS >= (ROWS ? 2 : 1) && (2 * NS - 1) * NLW <= 63, "tiles");
 };
 
@@ -532,6 +557,7 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
     __shared__ float st_m[NP][M16], st_l[NP][M16], fin[M16];
     __shared__ Plan plan;
     __shared__ int odd_any;                                // some edge value was not finite
+    __shared__ i32x4 q_lds[S::QL > 0 ? S::QL * NC * 64 : 1];
     const Cache& C = A.c;
     const int t = static_cast<int>(threadIdx.x), lane = t & 63, wv = __builtin_amdgcn_readfirstlane(t >> 6);
     const int r16 = lane & 15, g = lane >> 4;
@@ -585,7 +611,7 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
             recs[A.direct ? b : w] = RangeRec{b, n_tok, ranges.holding(pre), ranges.holding(pre + units - 1)};
         first = false;
         if (n_tok == 0) {                                  // bad lengths: one unit, NaN
-            for (int i = t; i < M16 * D; i += NTQ) {
+            for (int i = fresh(t); i < M16 * D; i += NTQ) {
                 const int m = m0 + i / D;
                 if (m < A.M) {
                     const long long row = (static_cast<long long>(b) * C.R + m / A.G) * A.Hq + h * A.G + m % A.G;
@@ -628,12 +654,13 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
                                                      16, 0, NT_LOAD);
                 }
             } else {
+                const int l = fresh(lane), lrow = l / S::CPR;
 #pragma unroll 1
                 for (int j = j0; j < j0 + S::NLW; ++j) {
                     const int row = j * S::RPI + lrow;
                     const int page = __shfl(pages, row, 64);
                     const int slot = key_of(tile, row) & slot_mask;
-                    const char* src = cache + page * str[0] + slot * str[2] + ((lane % S::CPR) ^ S::mix(lrow)) * 16;
+                    const char* src = cache + page * str[0] + slot * str[2] + ((l % S::CPR) ^ S::mix(lrow)) * 16;
                     __builtin_amdgcn_global_load_lds((glb_ptr)src, untraced((lds_ptr)(dst + j * S::GAP)), 16, 0, NT_LOAD);
                 }
             }
@@ -656,24 +683,28 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
             pages = checked(p[AHEAD]);
         }
         // this lane's query rows: the MFMA's B operand, and where each one stands
-        i32x4 qf[MT][NC];
+        constexpr int REG_Q = MT - S::QL;                  // row tiles with their queries in registers
+        i32x4 qf[REG_Q][NC];
         int pos[MT];                                       // the row's position
         float slope[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const int m = m0 + mw + mt * 16 + r16;
-            const int i = m < A.M ? m / A.G : 0, hq = h * A.G + (m < A.M ? m % A.G : 0);
+            const int m = m0 + mw + mt * 16 + fresh(r16), G = fresh(A.G);
+            const int i = m < A.M ? m / G : 0, hq = h * G + (m < A.M ? m % G : 0);
             const char* row = A.q + b * A.qs[0] + i * A.qs[1] + hq * A.qs[2];
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 // the products with 8 bits take 16 consecutive elements of a key per lane
                 const int d = E4M3 ? (c / 2) * 64 + g * 16 + (c & 1) * 8 : c * 32 + g * 8;
-                qf[mt][c] = *reinterpret_cast<const i32x4*>(row + d * 2);
-                if (m >= A.M) qf[mt][c] = i32x4{0, 0, 0, 0};
+                i32x4 qv = *reinterpret_cast<const i32x4*>(row + d * 2);
+                if (m >= A.M) qv = i32x4{0, 0, 0, 0};
+                if (mt < REG_Q) qf[mt < REG_Q ? mt : 0][c] = qv;
+                else if (wv == 0) q_lds[((mt - REG_Q) * NC + c) * 64 + lane] = qv;
             }
             pos[mt] = kv + min(i, n_tok - 1);
             slope[mt] = A.slopes ? A.slopes[hq] * LOG2E : 0.0f;
         }
+        if constexpr (S::QL > 0) __syncthreads();
         f32x4 acc[ND][MT];
         float mx[MT], sum[MT];
 #pragma unroll
@@ -687,7 +718,7 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
         // become zeros; of those that only some rows see what is not finite does, and is
         // added to the rows that see it at the end.
         auto clean = [&](unsigned char* vt, int tok0, int from, int by) {
-            for (int c = from; c < KT * S::CPR; c += by) {
+            for (int c = fresh(from); c < KT * S::CPR; c += by) {
                 i32x4* at16 = reinterpret_cast<i32x4*>(vt + c / 64 * S::GAP + c % 64 * 16);
                 const int key = tok0 + c / S::CPR;
                 if (key < lo || key >= hi) {
@@ -744,6 +775,9 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
                     pages = checked(page_at(tile + (NS + 1) * NWQ));
                 }
             }
+            i32x4 qt[S::QL > 0 ? S::QL : 1][NC];
+#pragma unroll
+            for (int i = 0; i < S::QL * NC; ++i) qt[i / NC][i % NC] = q_lds[i * 64 + lane];
             f32x4 sc[2][MT];
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
@@ -759,7 +793,8 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
                         k = kf[a][c];
                     }
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) sc[a][mt] = mfma<T>(k, qf[mt][c], sc[a][mt]);
+                    for (int mt = 0; mt < MT; ++mt)
+                        sc[a][mt] = mfma<T>(k, mt < REG_Q ? qf[mt < REG_Q ? mt : 0][c] : qt[mt < REG_Q ? 0 : mt - REG_Q][c], sc[a][mt]);
                 }
             }
             // scores in units of log2, masked
@@ -797,7 +832,7 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
             if (A.slopes) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const int away = tok + 4 * g - pos[mt];
+                    const int away = tok + 4 * fresh(g) - pos[mt];
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         sc[j / 4][mt][j % 4] += slope[mt] * static_cast<float>(away + 16 * (j / 4) + j % 4);
@@ -806,7 +841,7 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
             if (edge) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const int away = tok + 4 * g - pos[mt];
+                    const int away = tok + 4 * fresh(g) - pos[mt];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int k = away + 16 * (j / 4) + j % 4;
@@ -945,18 +980,18 @@ __global__ __launch_bounds__(NTQ, (AttnShape<D, MT, E4M3, ROWS>::OCC)) void attn
             for (int d = 0; d < DC; ++d)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                    *reinterpret_cast<f32x4*>(ex + (((ROWS ? 0 : wv) * DC + d) * M16 + mw + mt * 16 + r16) * 16 + 4 * g) =
+                    *reinterpret_cast<f32x4*>(ex + (((ROWS ? 0 : wv) * DC + d) * M16 + mw + mt * 16 + fresh(r16)) * 16 + 4 * g) =
                         acc[d0 + d][mt];
             __syncthreads();
             if (t == 0) odd_any = 0;                       // (everyone has read it)
-            for (int i = t; i < M16 * DC * 4; i += NTQ) {
+            for (int i = fresh(t); i < M16 * DC * 4; i += NTQ) {
                 const int m = i / 4 % M16, block = d0 + i / (4 * M16), d = block * 16 + i % 4 * 4;
                 if (m0 + m >= A.M) continue;
                 f32x4 o = *reinterpret_cast<const f32x4*>(ex + 4 * i);
 #pragma unroll
                 for (int j = 1; j < NP; ++j) o += *reinterpret_cast<const f32x4*>(ex + j * M16 * DC * 16 + 4 * i);
                 if (odd) {
-                    const int at_pos = kv + min((m0 + m) / A.G, n_tok - 1);
+                    const int at_pos = kv + min((m0 + fresh(m)) / A.G, n_tok - 1);
                     const int from = max(beg, lo), past = min(stop, hi), seen_by_all = hi - A.window;
                     for (int key = from; key < past; ++key) {
                         if (key <= kv && (A.window <= 0 || key >= seen_by_all)) {
@@ -1547,11 +1582,11 @@ AttnPlan attn_plan(int B, int R, int Hq, int Hkv, int D, bool e4m3, int page_siz
     AttnPlan p;
     p.M = R * (Hq / Hkv);
     const int tiles = (p.M + 15) / 16;
-    // Up to 32 query rows the waves take keys each, beyond that rows each: with 48 rows and
-    // more a wave's accumulators leave only one wave to a SIMD (R * G = 40, 16 rows of 8192
-    // keys, bfloat16: 83 us by rows, 99 by keys at two waves to a SIMD, with spills). The
-    // exception are 8-bit caches, which every wave widens for itself: by rows that is four
-    // times the work (R * G = 40, 131071 keys: 74 us by rows, 67 by keys).
+    // Up to 32 query rows the waves take keys each, beyond that rows each: accumulators for 48
+    // rows leave a wave of 16-bit keys too few registers (R * G = 40, 16 rows of 8192 keys,
+    // bfloat16: 104.8 us by rows, 110.1 by keys with some queries in LDS). The exception are
+    // 8-bit caches, which every wave widens for itself: by rows that is four times the work
+    // (R * G = 40, 131071 keys: 74 us by rows, 65 by keys).
     p.rows = tiles > (e4m3 && D < 256 ? 3 : 2);
     p.MB = 1;
     p.MT = tiles;
