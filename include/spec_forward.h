@@ -57,8 +57,8 @@ extern "C" {
  *     b * stride[0] + i * stride[1] + h * stride[2] + j (elements; 16-byte aligned base,
  *     strides multiples of 8), e.g. slices of a fused projection's output.
  *   cache_dtype: dtype, or SPEC_DTYPE_E4M3 with k_scale, v_scale [Hkv] float32 (NULL
- *     otherwise): code = e4m3(x / scale[h]), the quotient in float32, then nearest with ties to even, saturating at
- *     +-448; NaN stays NaN.
+ *     otherwise): code = e4m3(x / scale[h]), the quotient in float32, then nearest with
+ *     ties to even, saturating at +-448; NaN stays NaN.
  * A batch row whose kv_len is negative, whose draft_len is outside [0, R - 1] or whose
  * tokens do not fit max_pages * page_size positions is not written; a token whose page is
  * outside [0, pages) is not written. Distinct tokens of a call must go to distinct cache
@@ -82,9 +82,10 @@ int spec_kv_append(const void* k, const int64_t* k_stride, const void* v, const 
  *   cap(x) = softcap * tanh(x / softcap), or x when softcap is 0; slopes NULL: no bias;
  *   window 0: no lower bound.
  *   q: [B, R, Hq, D], dtype bfloat16 or float16, with strides as k of spec_kv_append.
- *   out: [B, R, Hq, D] dense, of q's dtype, 16-byte aligned, fully overwritten: tokens
- *     behind draft_len's get zeros; a batch row with a bad kv_len or draft_len (as in
- *     spec_kv_append) or a page outside [0, pages) among those it needs gets NaN.
+ *   out: [B, R, Hq, D] dense, of q's dtype, 16-byte aligned, fully overwritten, not
+ *     overlapping q or the cache: tokens behind draft_len's get zeros; a batch row with a
+ *     bad kv_len or draft_len (as in spec_kv_append) or a page outside [0, pages) among
+ *     those it needs gets NaN.
  * Only cache places that a used token sees are used: pages before every window and behind
  * the last token may be unmapped, and NaN or infinities there change nothing.
  * Products of q and k are summed in float32, the softmax and the sums are float32; the
@@ -97,7 +98,8 @@ int spec_kv_append(const void* k, const int64_t* k_stride, const void* v, const 
  * initialisation needed, one call at a time. 1 <= R <= SPEC_MAX_K + 1,
  * 1 <= Hkv <= 1024, Hq a multiple of Hkv up to 1024, otherwise the limits of
  * spec_kv_append. Errors: as there, plus SPEC_ERR_VALUE (scale not finite, softcap
- * negative, not finite or below 1e-30 |scale| without being 0, window negative) and SPEC_ERR_WORKSPACE.
+ * negative, not finite or below 1e-30 |scale| without being 0, window negative) and
+ * SPEC_ERR_WORKSPACE.
  */
 int spec_attention(const void* q, const int64_t* q_stride, int dtype, int32_t B, int32_t R, int32_t Hq, int32_t Hkv,
                    int32_t D, const void* k_cache, const int64_t* k_cache_stride, const void* v_cache,

@@ -346,6 +346,11 @@ def test_attention_refusals(run):
     refused(f, a, window=-1)
     refused(f, a, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     refused(f, a, out=torch.empty((2, 2, 4, 64), device=DEV))
+    refused(f, a, window=2 ** 32 + 5)                      # 5, cut to 32 bits
+    dense = a["q"].contiguous()
+    refused(f, a, q=dense, out=dense)
+    refused(f, a, out=a["k_cache"].flatten()[:2 * 2 * 4 * 64].view(2, 2, 4, 64))
+    refused(f, a, page_table=torch.empty((2, 2 ** 31 + 3), dtype=torch.int32, device=DEV))
     e = dev(fc.make_attention(40, B=2, R=2, Hkv=2, G=2, D=64, cache="e4m3"))
     refused(f, e, k_scale=None)
     refused(f, e, v_scale=torch.ones(2, dtype=torch.float64, device=DEV))
@@ -370,6 +375,8 @@ def test_append_refusals(run):
 def test_adjust_refusals(run):
     a = dev(fc.make_adjust(42))
     f = tv.spec_adjust
+    with pytest.raises(ValueError):                        # 1000 columns, cut to 32 bits
+        f(torch.empty((1, 1, 2 ** 32 + 1000), dtype=torch.bfloat16, device=DEV))
     refused(f, a, logits=a["logits"].half())
     refused(f, a, logits=a["logits"][:, :, :999])
     refused(f, a, logits=a["logits"].cpu())

@@ -96,6 +96,12 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _check_sizes(bits: int) -> None:
+    """bits: the sizes that the library takes as int32, or-ed (ctypes would cut them)."""
+    if bits >> 31:
+        raise ValueError("a size is beyond 2^31 - 1")
+
+
 def _check(t, name: str, shape, dtype, dev: torch.device) -> None:
     """A dense tensor of this shape and dtype on dev."""
     try:
@@ -114,6 +120,20 @@ def _check_strided(t, name: str, es: int, dev: torch.device) -> None:
     if s[3] != 1 or t.data_ptr() % 16 or (s[0] | s[1] | s[2]) * es % 16:
         raise ValueError(f"{name} must be contiguous in its last dimension, with a 16-byte aligned start and "
                          f"strides that are multiples of 16 bytes (got strides {list(s)} of {es}-byte elements)")
+
+
+def _span(t: torch.Tensor) -> tuple:
+    """The bytes from t's first element to behind its last."""
+    at = t.data_ptr()
+    return at, at + (sum(s * (n - 1) for s, n in zip(t.stride(), t.shape)) + 1) * t.element_size()
+
+
+def _check_apart(out: torch.Tensor, name: str, **inputs) -> None:
+    a, b = _span(out)
+    for other, t in inputs.items():
+        c, d = _span(t)
+        if a < d and c < b:
+            raise ValueError(f"{name} overlaps {other}")
 
 
 def _overlaps_itself(t: torch.Tensor) -> bool:
@@ -149,6 +169,7 @@ def _check_cache(k_cache, v_cache, page_table, kv_len, draft_len, k_scale, v_sca
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 [B, max_pages] tensor")
     max_pages = page_table.shape[1]
+    _check_sizes(B | max_pages)
     _check(page_table, "page_table", (B, max_pages), torch.int32, dev)
     _check(kv_len, "kv_len", (B,), torch.int32, dev)
     if draft_len is not None:
@@ -188,6 +209,7 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
                                                           v_scale, B, D, dtype, dev)
     if H != Hkv:
         raise ValueError(f"k holds {H} heads, the cache {Hkv}")
+    _check_sizes(R)
     if _overlaps_itself(k_cache) or _overlaps_itself(v_cache):
         raise ValueError("k_cache and v_cache must hold every element at a place of its own")
     _call(forward_lib().spec_kv_append, dev, k.data_ptr(), _stride(k), v.data_ptr(), _stride(v), _QKV[dtype],
@@ -239,6 +261,8 @@ def spec_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     _check_strided(q, "q", 2, dev)
     Hkv, pages, page_size, max_pages, code = _check_cache(k_cache, v_cache, page_table, kv_len, draft_len, k_scale,
                                                           v_scale, B, D, dtype, dev)
+    if not 0 <= window <= 0x7fffffff:
+        raise ValueError(f"window must be in [0, 2^31 - 1] (got {window})")
     if slopes is not None:
         _check(slopes, "slopes", (Hq,), torch.float32, dev)
     if out is None:
@@ -247,6 +271,7 @@ def spec_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         _check(out, "out", shape, dtype, dev)
         if out.data_ptr() % 16:
             raise ValueError("out must be 16-byte aligned")
+        _check_apart(out, "out", q=q, k_cache=k_cache, v_cache=v_cache)
     key = (B, R, Hq, Hkv, D, code, page_size, max_pages)
     need = _need_cache.get(key)
     if need is None:
@@ -341,6 +366,7 @@ def spec_adjust(logits: torch.Tensor, tokens: Optional[torch.Tensor] = None, *,
         _check(admit_row, "admit_row", (B, R), torch.int32, dev)
     if draft_len is not None:
         _check(draft_len, "draft_len", (B,), torch.int32, dev)
+    _check_sizes(B | R | V | H | nb | n_admit)
     if out is None:
         dtype = kind if out_dtype is None else out_dtype
         if dtype != kind and dtype != torch.float32:
