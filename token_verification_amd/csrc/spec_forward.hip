@@ -231,7 +231,8 @@ struct AttnParams {
     int M;                     // R * G query rows per cache head
     int MB;                    // row blocks of M16 rows
     int M16;                   // query rows of a workgroup
-    int W;                     // workgroups per cache head and row block
+    int W;                     // workgroups per cache head and row block, at most
+    int one;                   // ... with one per CU (no more than W)
     int direct;                // join_kernel goes by batch row (else by border between ranges)
     int slices;                // join_kernel: threads that share a sequence's pieces
 };
@@ -341,8 +342,15 @@ __device__ inline long long uniform(long long x) {
     return static_cast<long long>(static_cast<unsigned long long>(static_cast<unsigned>(hi)) << 32 | lo);
 }
 
-__device__ inline Ranges cut(long long total, int most) {
+// At most A.W ranges, but one workgroup per CU (A.one) where that leaves no more than four
+// units to each, in sequences of more than 16 on average: fewer pieces then save more than a
+// second workgroup's loads gain (one row of 5 tokens, 8 x 4, D = 128: 8192 keys 20.9 us
+// against 25.6, 16384 keys 25.8 against 28.9). With shorter sequences the longer ranges take
+// parts of several, one after the other (4 rows of 1000 to 2000 keys: 25.1 us against 22.9;
+// 100 rows of 4 tokens, 150 keys: 40 against 30).
+__device__ inline Ranges cut(const AttnParams& A, long long total) {
     Ranges r;
+    const int most = total <= 4ll * A.one && total > 16ll * A.c.B ? A.one : A.W;
     r.ranges = total < most ? static_cast<int>(total) : most;
     if (total <= 0x7fffffff) {
         r.size = static_cast<int>(total) / r.ranges;
@@ -367,7 +375,7 @@ __device__ inline Ranges locate(const AttnParams& A, Plan& P, int w, int& b, int
             u = static_cast<unsigned>(seq_from(A, lkv, ln).units);
         }
         const unsigned inc = wave_inclusive(u);
-        const Ranges r = cut(uniform(static_cast<int>(__shfl(inc, 63, 64))), A.W);
+        const Ranges r = cut(A, uniform(static_cast<int>(__shfl(inc, 63, 64))));
         const unsigned target = static_cast<unsigned>(r.start(w));
         b = w < r.ranges ? uniform(__ffsll(__ballot(inc > target)) - 1) : 0;
         kv = uniform(__shfl(lkv, b, 64));
@@ -385,7 +393,7 @@ __device__ inline Ranges locate(const AttnParams& A, Plan& P, int w, int& b, int
         block_inclusive(P, b0 + t < B ? static_cast<unsigned>(seq_of(A, b0 + t).units) : 0u, sum);
         total += sum;
     }
-    const Ranges r = cut(uniform(total), A.W);
+    const Ranges r = cut(A, uniform(total));
     if (w >= r.ranges) return r;
     const long long target = r.start(w);
     long long run = 0;
@@ -1582,7 +1590,7 @@ int check_cache(int dtype, int32_t B, int32_t R, int32_t max_R, int32_t Hkv, int
 
 // Row blocks, ranges and workspace of an attention call.
 struct AttnPlan {
-    int M, MB, MT, M16, W;
+    int M, MB, MT, M16, W, one;
     bool rows;                 // the waves share the query rows (else the keys)
     size_t slots_at, bytes;
 };
@@ -1626,6 +1634,7 @@ AttnPlan attn_plan(int B, int R, int Hq, int Hkv, int D, bool e4m3, int page_siz
     const long long units = B * ((static_cast<long long>(max_pages) * page_size + 2 * TT + TU - 1) / TU);
     if (w > units) w = units;
     p.W = w < 1 ? 1 : static_cast<int>(w);
+    p.one = (CUS + lanes - 1) / lanes < p.W ? (CUS + lanes - 1) / lanes : p.W;
     p.slots_at = (p.W * sizeof(RangeRec) + 255) & ~static_cast<size_t>(255);
     p.bytes = p.slots_at + static_cast<size_t>(lanes) * p.W * 2 * p.M16 * (D + 2) * sizeof(float);
     p.bytes = p.W == 1 ? 256 : (p.bytes + 255) & ~static_cast<size_t>(255);
@@ -1767,7 +1776,7 @@ int spec_attention(const void* q, const int64_t* q_stride, int dtype, int32_t B,
     A.ws = static_cast<float*>(workspace);
     A.scale = scale; A.softcap = softcap; A.window = window;
     A.Hq = Hq; A.G = Hq / Hkv; A.D = D;
-    A.M = plan.M; A.MB = plan.MB; A.M16 = plan.M16; A.W = plan.W;
+    A.M = plan.M; A.MB = plan.MB; A.M16 = plan.M16; A.W = plan.W; A.one = plan.one;
     A.slots_at = static_cast<long long>(plan.slots_at / sizeof(float));
     A.direct = B < plan.W;
     // a sequence has about W / B pieces (one row of 8192 keys, W = 64: 22.5 us with eight
