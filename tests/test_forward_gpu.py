@@ -57,6 +57,8 @@ def test_append_e4m3_rounds_every_value(run, dtype):
     dict(B=2, R=4, Hkv=3, G=7, D=128, cache="e4m3", lens=[2048, 2047]), dict(B=300, lens=[(7 * b) % 40 for b in range(300)]),
     dict(B=2, R=3, Hkv=2, D=128, window=500, softcap=50.0, lens=[3001, 499], dtype="f16"),
     dict(B=1, Hkv=20, G=1, lens=[1500], slopes=True), dict(B=100, R=2, lens=[(97 * b) % 700 for b in range(100)]),
+    dict(B=1, Hkv=20, G=1, lens=[3000]), dict(B=2, R=2, Hkv=8, lens=[6000, 20]),
+    dict(B=1, R=5, Hkv=8, G=8, D=128, cache="e4m3", lens=[8000]), dict(B=3, Hkv=16, G=1, lens=[40, 7000, 0], window=6500),
     dict(B=600, Hkv=1, G=2, lens=[(131 * b) % 900 for b in range(600)]), dict(B=2, R=9, G=8, Hkv=2, D=128, lens=[2500, 60]),
     dict(B=2, R=6, G=7, Hkv=2, D=128, cache="e4m3", lens=[3000, 100]), dict(B=1, R=8, G=8, Hkv=1, D=256, lens=[1000]),
     dict(B=2, R=65, G=8, Hkv=1, D=128, lens=[700, 0]), dict(B=1, R=12, G=16, Hkv=1, D=128, lens=[3000], window=1000), dict(B=1, R=2, D=256, cache="e4m3", dtype="f16", lens=[1200], page=128),
